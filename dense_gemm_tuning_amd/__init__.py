@@ -34,7 +34,9 @@ GEMM_ERR_LAUNCH = -6
 GEMM_ERR_ARG = -7
 GEMM_ERR_WORKSPACE = -8
 GEMM_ERR_SCRATCH = -9
+GEMM_ERR_ALIGN = -10
 NOALLOC_SCRATCH_BYTES = 64 << 20  # DGT_GEMM_NOALLOC_SCRATCH_BYTES
+MX4_MAX_PITCH = 1 << 24  # DGT_GEMM_MX4_MAX_PITCH
 
 VARIANT_AUTO = 0
 VARIANT_NAIVE = 1
@@ -53,7 +55,9 @@ EXPORTS = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_f32_variant", "gemm_bf16_v
            "gemm_f16_variant", "gemm_ex", "gemm_strided_batched", "gemm_splitk",
            "gemm_splitk_noalloc", "gemm_splitk_slices", "gemm_splitk_workspace_size",
            "gemm_streamk", "gemm_streamk_workspace_size", "gemm_select_variant",
-           "gemm_status_string", "gemm_abi_version")
+           "gemm_status_string", "gemm_abi_version", "gemm_mx4_code_pitch",
+           "gemm_mx4_scale_pitch", "gemm_mx4_quantize", "gemm_mx4_dequantize", "gemm_mx4",
+           "gemm_mx4_a16", "gemm_orthogonalize", "gemm_orthogonalize_workspace_size")
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
@@ -107,6 +111,23 @@ def _load() -> ctypes.CDLL:
                                              p, i, i64, p, i64, i, p]
         lib.gemm_select_variant.restype = i
         lib.gemm_select_variant.argtypes = [i] * 9
+        for name in ("gemm_mx4_code_pitch", "gemm_mx4_scale_pitch"):
+            fn = getattr(lib, name)
+            fn.restype = i64
+            fn.argtypes = [i]
+        lib.gemm_mx4_quantize.restype = i
+        lib.gemm_mx4_quantize.argtypes = [i, i, i, i, p, i, p, i, p, i, p]
+        lib.gemm_mx4_dequantize.restype = i
+        lib.gemm_mx4_dequantize.argtypes = [i, i, i, p, i, p, i, p, i, p]
+        lib.gemm_mx4.restype = i
+        lib.gemm_mx4.argtypes = [i, i, i, f, p, i, p, i, p, i, p, i, f, p, i, p, p]
+        lib.gemm_mx4_a16.restype = i
+        lib.gemm_mx4_a16.argtypes = [i, i, i, i, f, p, i, p, i, p, i, f, p, i, p, p]
+        lib.gemm_orthogonalize.restype = i
+        lib.gemm_orthogonalize.argtypes = [i, i, i, p, i, i64, p, i, i64, i, i, f, f, f, f, p, i64,
+                                           p]
+        lib.gemm_orthogonalize_workspace_size.restype = i64
+        lib.gemm_orthogonalize_workspace_size.argtypes = [i, i, i]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [i]
         lib.gemm_abi_version.restype = i
@@ -202,6 +223,45 @@ def gemm_select_variant(dtype, trans_a, trans_b, M, N, K, lda, ldb, ldc) -> int:
                                        lda, ldb, ldc)
 
 
+def gemm_mx4_code_pitch(K) -> int:
+    return _load().gemm_mx4_code_pitch(K)
+
+
+def gemm_mx4_scale_pitch(K) -> int:
+    return _load().gemm_mx4_scale_pitch(K)
+
+
+def gemm_mx4_quantize(dtype, trans, M, K, X, ldx, Q, ldq, S, lds, stream=0) -> int:
+    return _load().gemm_mx4_quantize(int(dtype), int(trans), M, K, X, ldx, Q, ldq, S, lds, stream)
+
+
+def gemm_mx4_dequantize(dtype, M, K, Q, ldq, S, lds, Y, ldy, stream=0) -> int:
+    return _load().gemm_mx4_dequantize(int(dtype), M, K, Q, ldq, S, lds, Y, ldy, stream)
+
+
+def gemm_mx4(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc, bias=0,
+             stream=0) -> int:
+    return _load().gemm_mx4(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc,
+                            bias, stream)
+
+
+def gemm_mx4_a16(dtype, M, N, K, alpha, A, lda, B, ldb, SB, ldsb, beta, C, ldc, bias=0,
+                 stream=0) -> int:
+    return _load().gemm_mx4_a16(int(dtype), M, N, K, alpha, A, lda, B, ldb, SB, ldsb, beta, C, ldc,
+                                bias, stream)
+
+
+def gemm_orthogonalize(dtype, M, N, G, ldg, stride_g, O, ldo, stride_o, batch, steps, a, b, c, eps,
+                       workspace, workspace_bytes, stream=0) -> int:
+    return _load().gemm_orthogonalize(int(dtype), M, N, G, ldg, stride_g, O, ldo, stride_o, batch,
+                                      int(steps), a, b, c, eps, workspace, int(workspace_bytes),
+                                      stream)
+
+
+def gemm_orthogonalize_workspace_size(M, N, batch) -> int:
+    return _load().gemm_orthogonalize_workspace_size(M, N, batch)
+
+
 def gemm_status_string(status: int) -> str:
     return _load().gemm_status_string(status).decode()
 
@@ -227,14 +287,14 @@ def _ld(t) -> int:
 def _check_layout(named, dims=(2,)):
     """Structure checks of the torch-facing calls, run before anything reaches
     the library: each (name, tensor) has a dimension count in ``dims`` and,
-    unless it is empty, unit stride along its last axis (row-major rows).  A
-    column-strided view would otherwise pass the leading-dimension check and
+    unless it is empty or has a single column, unit stride along its last axis
+    (row-major rows).  A column-strided view would otherwise pass the leading-dimension check and
     read the wrong elements."""
     for name, t in named:
         if t.dim() not in dims:
             raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, "
                              f"got {t.dim()}")
-        if t.numel() > 0 and t.stride(-1) != 1:
+        if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must be row-major with unit column stride")
 
 
@@ -436,3 +496,179 @@ def gemm_stream(A, B, C, alpha: float = 1.0, beta: float = 0.0, workspace=None, 
     return gemm_streamk(dtype, trans_a, trans_b, M, N, K, float(alpha), A.data_ptr(), _ld(A),
                         B.data_ptr(), _ld(B), float(beta), C.data_ptr(), _ld(C), ws_ptr,
                         ws_bytes, _stream_handle(stream))
+
+
+def _float_code(t, name):
+    import torch
+    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    if t.dtype not in codes:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return codes[t.dtype]
+
+
+def _call_on(device, stream, call):
+    """call(stream handle) with ``device`` the current GPU and, by default,
+    the stream current there (a tensor may live on another GPU than the one
+    the caller has current)."""
+    import torch
+    if hasattr(stream, "device") and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        return call(_stream_handle(stream))
+
+
+def mx4_empty(rows: int, K: int, device="cuda"):
+    """Uninitialised storage of a rows x K MX4 operand: (codes, scales), two
+    uint8 tensors of the smallest row pitches."""
+    import torch
+    return (torch.empty(rows, gemm_mx4_code_pitch(K), dtype=torch.uint8, device=device),
+            torch.empty(rows, gemm_mx4_scale_pitch(K), dtype=torch.uint8, device=device))
+
+
+def _check_mx4(rows, K, Q, S, name):
+    """An MX4 operand of ``rows`` rows and K elements: uint8 codes
+    [rows, >= code pitch] and scales [rows, >= scale pitch]."""
+    import torch
+    if Q.dtype != torch.uint8 or S.dtype != torch.uint8:
+        raise TypeError(f"{name} codes and scales must be uint8")
+    _check_layout(((f"{name} codes", Q), (f"{name} scales", S)))
+    if Q.shape[0] != rows or S.shape[0] != rows:
+        raise ValueError(f"{name} codes and scales must have {rows} rows, got {Q.shape[0]} and "
+                         f"{S.shape[0]}")
+    if Q.shape[1] < gemm_mx4_code_pitch(K) or S.shape[1] < gemm_mx4_scale_pitch(K):
+        raise ValueError(f"{name}: {K} elements need rows of {gemm_mx4_code_pitch(K)} code and "
+                         f"{gemm_mx4_scale_pitch(K)} scale bytes, got {Q.shape[1]} and "
+                         f"{S.shape[1]}")
+
+
+def _pitch16(t) -> int:
+    """Row pitch of codes or scales; that of a single-row or empty operand is
+    never used, so report the next multiple of 16 bytes."""
+    return t.stride(0) if t.shape[0] > 1 and t.numel() > 0 else max(16, (t.shape[1] + 15) // 16 * 16)
+
+
+def quantize_mx4(X, Q, S, trans: bool = False, stream=None) -> int:
+    """(Q, S) <- op(X) in MX4 blocks along its columns (gemm_mx4_quantize);
+    op(X) is X, or X transposed when ``trans``.  X is float32, bfloat16 or
+    float16, row-major; Q and S as ``mx4_empty`` makes them for op(X).  Blocks run along
+    the summation index of the product the operand is for.  Returns the status
+    code."""
+    dtype = _float_code(X, "X")
+    _check_layout((("X", X),))
+    M, K = X.shape[::-1] if trans else X.shape
+    _check_mx4(M, K, Q, S, "Q, S:")
+    _check_device((("X", X), ("Q", Q), ("S", S)), Q.device)
+    if M == 0 or K == 0:
+        return GEMM_OK
+    return _call_on(Q.device, stream, lambda s: gemm_mx4_quantize(
+        dtype, trans, M, K, X.data_ptr(), _ld(X), Q.data_ptr(), _pitch16(Q), S.data_ptr(),
+        _pitch16(S), s))
+
+
+def dequantize_mx4(Q, S, Y, stream=None) -> int:
+    """Y [rows, K] <- the values of an MX4 operand (gemm_mx4_dequantize), Y
+    float32, bfloat16 or float16, row-major.  Returns the status code."""
+    dtype = _float_code(Y, "Y")
+    _check_layout((("Y", Y),))
+    M, K = Y.shape
+    _check_mx4(M, K, Q, S, "Q, S:")
+    _check_device((("Q", Q), ("S", S), ("Y", Y)), Y.device)
+    if M == 0 or K == 0:
+        return GEMM_OK
+    return _call_on(Y.device, stream, lambda s: gemm_mx4_dequantize(
+        dtype, M, K, Q.data_ptr(), _pitch16(Q), S.data_ptr(), _pitch16(S), Y.data_ptr(), _ld(Y),
+        s))
+
+
+def gemm_quantized(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=None,
+                   stream=None) -> int:
+    """C <- alpha*A*B^T + beta*C + bias with B an MX4 operand of N rows (codes
+    B, scales SB) and A either one of M rows (codes A, scales SA: gemm_mx4) or
+    a bfloat16 / float16 [M, K] tensor with SA None (gemm_mx4_a16).  C is
+    float32 [M, N], row-major; bias None or float32 [N].  With MX4 A the
+    summation runs over every stored element: codes past a ragged K are zeros
+    (quantize_mx4 writes them so).  Returns the status code."""
+    import torch
+    if C.dtype != torch.float32:
+        raise TypeError("C must be float32")
+    _check_layout((("A", A), ("C", C)))
+    M, N = C.shape
+    named = [("A", A), ("B", B), ("SB", SB), ("C", C)]
+    if SA is None:
+        if A.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("A must be bfloat16 or float16, or MX4 codes with their scales SA")
+        K = A.shape[1]
+        if A.shape[0] != M:
+            raise ValueError(f"shape mismatch: A {tuple(A.shape)}, C {tuple(C.shape)}")
+    else:
+        K = 2 * min(A.shape[1], B.shape[1])
+        if gemm_mx4_code_pitch(K) != 16 * (K // 32) or A.shape[1] != B.shape[1]:
+            raise ValueError("A and B must have code rows of one length, a multiple of 16 bytes, "
+                             f"got {A.shape[1]} and {B.shape[1]}")
+        _check_mx4(M, K, A, SA, "A, SA:")
+        named.append(("SA", SA))
+    _check_mx4(N, K, B, SB, "B, SB:")
+    bias_ptr = 0
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.dim() != 1 or bias.shape[0] != N:
+            raise ValueError("bias must be float32 [N]")
+        _check_layout((("bias", bias),), dims=(1,))
+        named.append(("bias", bias))
+        bias_ptr = bias.data_ptr()
+    _check_device(named, C.device)
+    if M == 0 or N == 0:
+        return GEMM_OK
+    tail = (B.data_ptr(), _pitch16(B), SB.data_ptr(), _pitch16(SB), float(beta), C.data_ptr(),
+            _ld(C), bias_ptr)
+    if SA is None:
+        return _call_on(C.device, stream, lambda s: gemm_mx4_a16(
+            _float_code(A, "A"), M, N, K, float(alpha), A.data_ptr(), _ld(A), *tail, s))
+    return _call_on(C.device, stream, lambda s: gemm_mx4(
+        M, N, K, float(alpha), A.data_ptr(), _pitch16(A), SA.data_ptr(), _pitch16(SA), *tail, s))
+
+
+def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7, workspace=None, stream=None) -> int:
+    """O <- G orthogonalised by ``steps`` Newton-Schulz steps
+    X <- a*X + (b*S + c*S*S)*X from X = G / (|G| + eps) (gemm_orthogonalize;
+    the default coefficients are the quintic's that Muon uses).  G is float32,
+    bfloat16 or float16 and O bfloat16, both [M, N] or [batch, M, N] with
+    row-major matrices; O may be G.  ``workspace`` is a contiguous GPU tensor
+    of at least gemm_orthogonalize_workspace_size bytes that no other call uses at
+    the same time; when None one is allocated here with torch, for the stream
+    the work runs on.  Returns the status code."""
+    import torch
+    dtype = _float_code(G, "G")
+    if O.dtype != torch.bfloat16:
+        raise TypeError("O must be bfloat16")
+    _check_layout((("G", G), ("O", O)), dims=(2, 3))
+    if G.shape != O.shape:
+        raise ValueError(f"shape mismatch: G {tuple(G.shape)}, O {tuple(O.shape)}")
+    named = [("G", G), ("O", O)]
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        named.append(("workspace", workspace))
+    _check_device(named, O.device)
+    if G.numel() == 0:
+        return GEMM_OK
+    M, N = G.shape[-2:]
+    batch = G.shape[0] if G.dim() == 3 else 1
+
+    def mat(t):
+        return (t[0], t.stride(0) if batch > 1 else 0) if t.dim() == 3 else (t, 0)
+
+    (G2, sg), (O2, so) = mat(G), mat(O)
+    need = gemm_orthogonalize_workspace_size(M, N, batch)
+    if need < 0:
+        return need
+    if workspace is None:
+        with torch.cuda.device(O.device):
+            handle = _stream_handle(stream)
+            on = torch.cuda.ExternalStream(handle, device=O.device) if stream is not None else None
+            with torch.cuda.stream(on):
+                workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
+    a, b, c = (float(v) for v in coefficients)
+    return _call_on(O.device, stream, lambda s: gemm_orthogonalize(
+        dtype, M, N, G2.data_ptr(), _ld(G2), sg, O2.data_ptr(), _ld(O2), so, batch, steps, a, b, c,
+        float(eps), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))

@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "../../include/dgt_gemm.h"
+#include "api_common.hpp"
 #include "gemm_common.hpp"
 
 static_assert(dgt::kScratchBytes == DGT_GEMM_NOALLOC_SCRATCH_BYTES,
@@ -18,12 +19,7 @@ static_assert(dgt::kScratchBytes == DGT_GEMM_NOALLOC_SCRATCH_BYTES,
 namespace {
 
 using dgt::GemmParams;
-
-enum class DType { F32, BF16, F16 };
-
-int elem_size(DType t) { return t == DType::F32 ? 4 : 2; }
-
-bool valid_flag(int f) { return f == 0 || f == 1; }
+using namespace dgt::api;
 
 // Flag, shape and leading-dimension checks (no pointers involved).  A is
 // stored M x K (ta == 0) or K x M (ta == 1); B is stored K x N (tb == 0) or
@@ -35,12 +31,6 @@ int check_shape(int ta, int tb, int M, int N, int K, int lda, int ldb, int ldc) 
         ldc < std::max(1, N))
         return GEMM_ERR_LD;
     return GEMM_OK;
-}
-
-// Bytes spanned by a rows x cols row-major operand with leading dim ld.
-uint64_t span_bytes(int rows, int cols, int ld, int esz) {
-    if (rows == 0 || cols == 0) return 0;
-    return ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)esz;
 }
 
 // The rung AUTO resolves to; the alpha == 0 / K == 0 case is handled before.
@@ -70,20 +60,6 @@ struct Call {
     void* stream;
     int k_last = 0;  // K of the last problem when > 0 (a split-K tail slice)
 };
-
-// [lo, hi) byte range covered by `batch` problems of `span` bytes, `stride`
-// bytes apart (empty when span == 0).
-struct Range {
-    uintptr_t lo, hi;
-};
-Range batch_range(const void* base, uint64_t span, int64_t stride_bytes, int batch) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(base);
-    if (span == 0 || batch <= 0) return {b, b};
-    return {b, b + (uint64_t)(batch - 1) * (uint64_t)stride_bytes + span};
-}
-bool overlaps(const Range& x, const Range& y) {
-    return x.lo < x.hi && y.lo < y.hi && x.lo < y.hi && y.lo < x.hi;
-}
 
 // Largest gridDim.y of one launch; longer batches take several launches.
 constexpr int kMaxBatchPerLaunch = 65535;
@@ -132,12 +108,6 @@ hipError_t dispatch(DType t, int variant, const GemmParams& p, bool reads_ab, hi
             return hipErrorInvalidConfiguration;
     }
 }
-
-// Strides beyond this (in elements) cannot describe device memory; rejecting
-// them keeps the range arithmetic below from overflowing.
-constexpr int64_t kMaxStride = int64_t(1) << 48;
-
-bool valid_stride(int64_t s) { return s >= 0 && s < kMaxStride; }
 
 int run(const Call& c) {
     if (c.batch < 0 || !valid_stride(c.stride_a) || !valid_stride(c.stride_b) ||
@@ -271,12 +241,6 @@ SplitPlan plan_splitk(DType t, int M, int N, int K, int requested) {
     const int splits = (K + kc - 1) / kc;
     if (splits <= 1) return {1, K};
     return {splits, kc};
-}
-
-bool dtype_of(int dtype, DType& t) {
-    if (dtype < GEMM_DTYPE_F32 || dtype > GEMM_DTYPE_F16) return false;
-    t = dtype == GEMM_DTYPE_F32 ? DType::F32 : dtype == GEMM_DTYPE_BF16 ? DType::BF16 : DType::F16;
-    return true;
 }
 
 // Both split-K entry points.  noalloc: the partials go to the library's fixed
@@ -501,6 +465,7 @@ const char* gemm_status_string(int status) {
         case GEMM_ERR_ARG: return "GEMM_ERR_ARG: unknown dtype or transpose flag, negative batch, splits or size, or stride out of range";
         case GEMM_ERR_WORKSPACE: return "GEMM_ERR_WORKSPACE: workspace missing or smaller than gemm_splitk_workspace_size";
         case GEMM_ERR_SCRATCH: return "GEMM_ERR_SCRATCH: gemm_splitk_noalloc: the partials (slices x M x N x 4 bytes) exceed the library's fixed scratch of DGT_GEMM_NOALLOC_SCRATCH_BYTES";
+        case GEMM_ERR_ALIGN: return "GEMM_ERR_ALIGN: MX4 codes or scales, or a workspace, not on 16-byte boundaries (base and row pitch)";
         default: return "unknown gemm status";
     }
 }

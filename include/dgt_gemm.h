@@ -66,6 +66,8 @@
 extern "C" {
 #endif
 
+/* Entry points may be added without a new version; the ones of a version keep
+ * their meaning. */
 #define DGT_GEMM_ABI_VERSION 9
 
 /* Input formats (the dtype argument of gemm_ex and gemm_select_variant). */
@@ -90,9 +92,13 @@ enum gemm_status {
                                    outside [0, 2^48)                         */
     GEMM_ERR_WORKSPACE = -8,    /* gemm_splitk: workspace NULL or smaller
                                    than gemm_splitk_workspace_size           */
-    GEMM_ERR_SCRATCH = -9       /* gemm_splitk_noalloc: the shape's partials
+    GEMM_ERR_SCRATCH = -9,      /* gemm_splitk_noalloc: the shape's partials
                                    (gemm_splitk_workspace_size) exceed
                                    DGT_GEMM_NOALLOC_SCRATCH_BYTES            */
+    GEMM_ERR_ALIGN = -10        /* MX4 codes or scales whose base or row
+                                   pitch is not a multiple of 16 bytes, or a
+                                   gemm_orthogonalize workspace whose base
+                                   is not                                    */
 };
 
 /* Kernel ladder (for measurement and tests; GEMM_VARIANT_AUTO is what
@@ -304,6 +310,112 @@ int gemm_streamk(int dtype, int trans_a, int trans_b, int M, int N, int K,
 /* Bytes of workspace gemm_streamk needs for this shape (0 when the call
  * runs as gemm_ex), or a negative status for bad arguments.  Host only. */
 int64_t gemm_streamk_workspace_size(int dtype, int M, int N, int K);
+
+/* ------------------------------------------------------------------ MX4
+ *
+ * Microscaled 4-bit operands (the MXFP4 format of the OCP Microscaling
+ * Formats specification 1.0).  A row of K elements is cut into blocks of 32
+ * consecutive k; element k stands for
+ *
+ *     value(code) * 2^(s - 127)
+ *
+ * with s the block's scale byte (255 stands for NaN: the whole block is NaN)
+ * and code 4 bits: bit 3 the sign, bits 2..0 one of the magnitudes 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6.  Storage of an M x K operand, two byte arrays:
+ *     codes   row i at Q + i*ldq, k in the low (k even) or high (k odd) half
+ *             of byte k/2; ldq >= gemm_mx4_code_pitch(K) = 16*ceil(K/32)
+ *             bytes.  The codes of k >= K in the last block are zero.
+ *     scales  row i at S + i*lds, block k/32 at byte k/32;
+ *             lds >= gemm_mx4_scale_pitch(K) = 16*ceil(K/512) bytes.  The
+ *             bytes past block (K-1)/32 are never used.
+ * Pitches and bases are multiples of 16 bytes (GEMM_ERR_ALIGN otherwise), and
+ * pitches at most DGT_GEMM_MX4_MAX_PITCH (a pitch outside the two limits is
+ * GEMM_ERR_LD; K is so limited to 2^25).  Blocks always run along the
+ * summation index, so both operands of a product are stored with k
+ * contiguous: A as M x K, B as N x K (a linear layer's weight as it is).  The
+ * three products of a training step of Y = X*W^T take the operands quantised
+ * along their own summation index (gemm_mx4_quantize with trans = 1 reads
+ * the stored transpose): X and W along [in]; G and W^T along [out]; G^T and
+ * X^T along the batch.
+ *
+ * Checks run in this order: dtype and flags, dimensions, pitches, quick
+ * return for an empty result, null pointers, alignment, overlap. */
+
+#define DGT_GEMM_MX4_MAX_PITCH (1 << 24)
+
+/* Smallest row pitches in bytes for K elements (0 for K <= 0).  Host only. */
+int64_t gemm_mx4_code_pitch(int K);
+int64_t gemm_mx4_scale_pitch(int K);
+
+/* Q, S <- the M x K matrix op(X) quantised: op(X)(i,k) = X[i*ldx + k]
+ * (trans = 0, X stored M x K) or X[k*ldx + i] (trans = 1, X stored K x M);
+ * X in the input format `dtype`, any alignment.  Per block: with amax the
+ * largest magnitude, e = floor(log2(amax)) - 2 clamped to [-127, 127] (-127
+ * when amax = 0) and s = e + 127; each element x becomes the code nearest to
+ * x * 2^-e, ties to the even code, magnitudes above 6 to 6.  A block that
+ * holds an infinity or a NaN gets s = 255 and zero codes.  The codes past K
+ * in the last block are written as zeros, and the scale bytes past the last
+ * block up to gemm_mx4_scale_pitch(K) as 127; nothing past those pitches is
+ * written. */
+int gemm_mx4_quantize(int dtype, int trans, int M, int K, const void* X, int ldx,
+                      uint8_t* Q, int ldq, uint8_t* S, int lds, void* stream);
+
+/* Y (M x K, row pitch ldy elements, format `dtype`) <- the values of Q, S.
+ * FP32 and BF16 hold every value exactly (a block's 6 * 2^127 and its like
+ * overflow to infinity); FP16 is rounded to nearest even. */
+int gemm_mx4_dequantize(int dtype, int M, int K, const uint8_t* Q, int ldq,
+                        const uint8_t* S, int lds, void* Y, int ldy, void* stream);
+
+/* C <- alpha*A*B^T + beta*C + bias with MX4 A (M x K; codes A, scales SA) and
+ * B (N x K; codes B, scales SB), fp32 accumulate and output; bias is NULL or
+ * N floats added to every row of C, unscaled.  alpha == 0 or K == 0 reads
+ * neither operand. */
+int gemm_mx4(int M, int N, int K, float alpha, const uint8_t* A, int lda,
+             const uint8_t* SA, int ldsa, const uint8_t* B, int ldb,
+             const uint8_t* SB, int ldsb, float beta, float* C, int ldc,
+             const float* bias, void* stream);
+
+/* The same with 16-bit A (GEMM_DTYPE_BF16 or GEMM_DTYPE_F16, M x K, row pitch
+ * lda elements, any alignment) against MX4 B: the products of a 16-bit and a
+ * 4-bit value are exact and summed in fp32. */
+int gemm_mx4_a16(int dtype, int M, int N, int K, float alpha, const uint16_t* A,
+                 int lda, const uint8_t* B, int ldb, const uint8_t* SB, int ldsb,
+                 float beta, float* C, int ldc, const float* bias, void* stream);
+
+/* ------------------------------------------------------- orthogonalisation
+ *
+ * O_z <- NS(G_z) for z = 0 .. batch-1: the M x N matrix G_z moved towards the
+ * nearest matrix with orthonormal rows (M <= N) or columns (M > N) by `steps`
+ * Newton-Schulz steps, as optimisers that orthogonalise a weight's update do:
+ *
+ *     X <- G / (|G|_F + eps)
+ *     steps times:  M <= N:  S = X*X^T,  X <- a*X + (b*S + c*S*S)*X
+ *                   M > N:   S = X^T*X,  X <- a*X + X*(b*S + c*S*S)
+ *
+ * G in the format `dtype` (row pitch ldg, problem stride stride_g elements),
+ * O as raw bf16 bits (ldo, stride_o).  The norm is summed in 64 bits.  The
+ * products take FP16 operands (scaled by powers of two into its range) and
+ * sum in fp32; X itself is carried in two FP16 halves of together 22 bits,
+ * and the term a*X uses both, so the result differs from the exact iteration
+ * by little more than its own rounding to bf16.  Coefficients for which the
+ * iterates' singular values stay below about 4 keep every intermediate in
+ * range.  A matrix holding an infinity or a NaN gives NaN.
+ *
+ * The workspace (device memory, 16-byte aligned, at least
+ * gemm_orthogonalize_workspace_size bytes) must not overlap G or O and must
+ * stay untouched until the work on `stream` has finished; calls that may run
+ * at the same time (other streams, captured graphs) need workspaces of their
+ * own.  G is read completely before O is written, so O may be G's memory.
+ * The problems' O ranges must be disjoint. steps must be
+ * 1 to 64, a, b, c finite and eps >= 0; batch 1 to 65535 (0 does nothing). */
+int gemm_orthogonalize(int dtype, int M, int N, const void* G, int ldg,
+                       int64_t stride_g, uint16_t* O, int ldo, int64_t stride_o,
+                       int batch, int steps, float a, float b, float c, float eps,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gemm_orthogonalize needs (0 for an empty call), or a
+ * negative status for negative arguments.  Host only. */
+int64_t gemm_orthogonalize_workspace_size(int M, int N, int batch);
 
 /* The rung GEMM_VARIANT_AUTO picks for this call (dtype: enum gemm_dtype;
  * trans_a, trans_b as for gemm_ex), or a negative status if the arguments
