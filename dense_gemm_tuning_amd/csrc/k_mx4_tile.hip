@@ -1,0 +1,325 @@
+// k_mx4_tile.hip -- products of two microscaled 4-bit operands on the matrix
+// cores: C <- alpha*A*B^T + beta*C + bias, both operands stored with k
+// contiguous.
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 with 4-bit operands takes, per lane, one
+// 16-byte chunk of codes (32 consecutive k of one row: a whole block) and one
+// scale byte, and multiplies blocks by 2^(sa + sb - 254) inside the sum.  A
+// chunk is as many bytes as the eight 16-bit elements of a lane of the
+// 32x32x16 product, and the instruction takes as long, so the kernel is the
+// k-contiguous form of the 16-bit tile kernel (mfma16_tile.hpp: operands
+// copied by DMA in pairs of 64-byte slices, 2 x 2 wavefronts, waits counted
+// in copies) with a chunk for eight elements: four times the k per byte, and
+// per second.  Its operand class is used as it is, on rows of 8*ceil(K/32)
+// "elements".
+//
+// Scales: a group of four slices is 16 blocks, 16 scale bytes per row of
+// each operand.  One copy instruction brings 64 rows of them into LDS, two
+// per wave and group (one at 128 x 128), issued after the barrier of the
+// group's first slice and needed at the barrier of its last; at the start of a
+// group every lane reads the 16 bytes of its rows once (TM reads per
+// operand) and keeps them in registers, so one LDS buffer serves.
+// Step s of slice J multiplies chunks 2s + h (h the half of the wave): its
+// byte is 2s + h of dword J, which a shift by 8h brings to byte 2s for every
+// lane, selected by the instruction.
+#include "mfma16_tile.hpp"
+#include "mx4.hpp"
+
+namespace dgt {
+namespace mx4 {
+
+namespace {
+
+using namespace mfma16;
+
+typedef int intx8 __attribute__((ext_vector_type(8)));
+
+// 4-bit operands occupy the first four of the eight operand registers.
+__device__ __forceinline__ intx8 widen(u32x4 x) {
+    return intx8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+}
+
+constexpr int kFp4 = 4;  // operand format code of E2M1
+
+// One wave's copies of a group's scales: 64 rows of an operand per copy.
+struct ScaleCopy {
+    const uint8_t* base;
+    uint32_t range, voff, at;  // at: byte offset in the LDS buffer
+
+    // rows row0 .. row0+63 of an operand of `rows` rows; `groups` 16-byte
+    // pieces per row; `lds_row`: first row's place in the buffer.
+    __device__ void init(const uint8_t* S, int64_t lds, int row0, int rows, int groups, int lds_row,
+                         int lane) {
+        const int n = min(64, rows - row0);
+        base = S + (int64_t)row0 * lds;
+        range = n <= 0 ? 0u : (uint32_t)((int64_t)(n - 1) * lds + 16 * (int64_t)groups);
+        voff = (uint32_t)(lane * lds);
+        at = 16 * lds_row;
+    }
+    __device__ void copy(uint8_t* buf, int g) const {
+        dma16(base, range, buf + at, voff + 16u * (uint32_t)g, 0);
+    }
+};
+
+template <int R, bool kEdge, bool kTail>
+__global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p, int tiles_m,
+                                                                      int tiles_n, int nb,
+                                                                      int grouped) {
+    constexpr int TM = Geo<R>::TM;
+    using Op = KcOperand<R>;
+    constexpr int CKC = Op::kHalfCopies;
+    constexpr int SC = R == 256 ? 2 : 1;  // scale copies per wave and group
+    __shared__ __attribute__((aligned(1024))) uint8_t sA0[Op::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t sA1[Op::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t sB0[Op::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t sB1[Op::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t sS[2 * R * 16];  // rows of A, then of B
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1, h = lane >> 5;
+    const TileIdx tile = xcd_tile(tiles_m, tiles_n, grouped != 0);
+    const int m0 = tile.bm * R, n0 = tile.bn * R;
+    const int ku = 8 * nb;                  // row length in 16-bit units
+    const int nk = (ku + BK - 1) / BK;      // slices of four blocks
+    const int groups = (nb + 15) / 16;
+
+    Op opa, opb;
+    opa.template init<kEdge>(static_cast<const uint16_t*>(p.A), p.lda / 2, m0, wm, wave, lane, nk,
+                             p.M, ku);
+    opb.template init<kEdge>(reinterpret_cast<const uint16_t*>(p.B), p.ldb / 2, n0, wn, wave, lane,
+                             nk, p.N, ku);
+    ScaleCopy sc[SC];
+    if constexpr (R == 256) {
+        sc[0].init(p.SA, p.ldsa, m0 + 64 * wave, p.M, groups, 64 * wave, lane);
+        sc[1].init(p.SB, p.ldsb, n0 + 64 * wave, p.N, groups, R + 64 * wave, lane);
+    } else {
+        const int half = 64 * (wave & 1);
+        if (wave < 2) sc[0].init(p.SA, p.ldsa, m0 + half, p.M, groups, half, lane);
+        else sc[0].init(p.SB, p.ldsb, n0 + half, p.N, groups, R + half, lane);
+    }
+
+    floatx16 acc[TM][TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    auto frags = [&](auto Jc, int s, u32x4 (&a)[TM], u32x4 (&b)[TM]) {
+        constexpr int J = decltype(Jc)::value;
+        opa.frags(pick<J / 2>(sA0, sA1, sA0, sA0), J % 2, s, a);
+        opb.frags(pick<J / 2>(sB0, sB1, sB0, sB0), J % 2, s, b);
+    };
+    auto copy_scales = [&](int g) {
+        g = g < groups ? g : groups - 1;  // past the end: the last group, never used
+#pragma unroll
+        for (int i = 0; i < SC; ++i) sc[i].copy(sS, g);
+    };
+    // The scales of group g for this lane's rows.  Blocks at or past nb (in
+    // the last group) get the neutral scale 1; their codes are masked.
+    u32x4 sa[TM], sb[TM];
+    const int srow_a = 16 * (wm * (R / 2) + (lane & 31));
+    const int srow_b = 16 * (R + wn * (R / 2) + (lane & 31));
+    auto read_scales = [&](int g) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            sa[t] = *reinterpret_cast<const u32x4*>(sS + srow_a + 512 * t);
+            sb[t] = *reinterpret_cast<const u32x4*>(sS + srow_b + 512 * t);
+        }
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                sa[t][d] >>= 8 * h;
+                sb[t][d] >>= 8 * h;
+            }
+        if constexpr (kTail) {
+            if (16 * (g + 1) > nb) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int left = nb - (16 * g + 4 * d + h);  // blocks from byte 0 on
+                    const uint32_t keep = left <= 0 ? 0u : left <= 2 ? 0xffffu : 0xffffffffu;
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) {
+                        sa[t][d] = (sa[t][d] & keep) | (0x7f7f7f7fu & ~keep);
+                        sb[t][d] = (sb[t][d] & keep) | (0x7f7f7f7fu & ~keep);
+                    }
+                }
+            }
+        }
+    };
+
+    // The products of step kS of slice kJ on (a, b); LDS reads and copies
+    // are spread between them as in the 16-bit kernel, kReads of 16 bytes per
+    // four products.
+    auto mfma_step = [&](auto Jc, auto Sc, auto Rc, const u32x4 (&a)[TM], const u32x4 (&b)[TM]) {
+        constexpr int J = decltype(Jc)::value, kS = decltype(Sc)::value, kReads = decltype(Rc)::value;
+#pragma unroll
+        for (int ti = 0; ti < TM; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TM; ++tj)
+                acc[ti][tj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    widen(a[ti]), widen(b[tj]), acc[ti][tj], kFp4, kFp4, 2 * kS, (int)sa[ti][J],
+                    2 * kS, (int)sb[tj][J]);
+        if constexpr (TM == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
+                    if (m < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
+                    if (m & 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);          // copy
+                }
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < TM * TM; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // copy
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    u32x4 a0[TM], b0[TM], a1[TM], b1[TM];
+    // In a slice cut by the row's end the chunks at or past nb hold whatever
+    // follows in the row; they are cleared (step s: chunk 4kt + 2s + h).
+    auto mask_k = [&](int kt, int s, u32x4 (&f)[TM]) {
+        const uint32_t keep = 4 * kt + 2 * s + h < nb ? 0xffffffffu : 0u;
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[t][e] &= keep;
+    };
+    // Slice kt at position J of its group: the copies, waits and barrier of the
+    // 16-bit kernel with both operands k-contiguous (even slices copy the second half of
+    // the next pair before the barrier, odd ones the first half of the pair
+    // after it behind the barrier), plus the next group's scales after the
+    // barrier of slice 0: newer than what slice 1's barrier publishes, so its
+    // wait lets them through; slice 2's wait covers them.
+    auto slice = [&](auto Jc, int kt, auto maskc) {
+        constexpr int J = decltype(Jc)::value;
+        constexpr bool kEven = J % 2 == 0;
+        constexpr bool kMask = decltype(maskc)::value;
+        using Two = std::integral_constant<int, 2>;
+        frags(Jc, 1, a1, b1);
+        if constexpr (kMask) {
+            if (kt == nk - 1 && nb % 4 != 0) {
+                mask_k(kt, 0, a0); mask_k(kt, 1, a1);
+                mask_k(kt, 0, b0); mask_k(kt, 1, b1);
+            }
+        }
+        if constexpr (kEven) {
+            opa.template copy<kEdge, kTail>(pick<(J / 2 + 1) % 2>(sA0, sA1, sA0, sA0), kt / 2 + 1, 1, wave);
+            opb.template copy<kEdge, kTail>(pick<(J / 2 + 1) % 2>(sB0, sB1, sB0, sB0), kt / 2 + 1, 1, wave);
+        }
+        mfma_step(Jc, std::integral_constant<int, 0>{}, Two{}, a0, b0);
+        DMA_WAIT_VMCNT_LGKM0((copies_after<true, true, kEven>(CKC, 0) + (J == 1 ? SC : 0)));
+        barrier();
+        frags(std::integral_constant<int, (J + 1) % 4>{}, 0, a0, b0);
+        if constexpr (J == 0) copy_scales(kt / 4 + 1);
+        if constexpr (!kEven) {
+            opa.template copy<kEdge, kTail>(pick<((J + 3) / 2) % 2>(sA0, sA1, sA0, sA0), (kt + 3) / 2, 0, wave);
+            opb.template copy<kEdge, kTail>(pick<((J + 3) / 2) % 2>(sB0, sB1, sB0, sB0), (kt + 3) / 2, 0, wave);
+        }
+        mfma_step(Jc, std::integral_constant<int, 1>{}, Two{}, a1, b1);
+        if constexpr (J == 3) read_scales(kt / 4 + 1);
+    };
+
+    copy_scales(0);
+    opa.template copy<kEdge, kTail>(sA0, 0, 0, wave);
+    opa.template copy<kEdge, kTail>(sA0, 0, 1, wave);
+    opb.template copy<kEdge, kTail>(sB0, 0, 0, wave);
+    opb.template copy<kEdge, kTail>(sB0, 0, 1, wave);
+    opa.template copy<kEdge, kTail>(sA1, 1, 0, wave);
+    opb.template copy<kEdge, kTail>(sB1, 1, 0, wave);
+    DMA_WAIT_VMCNT((prologue_after<true, true>(CKC, 0)));  // slice 0 and its scales landed
+    barrier();
+    frags(std::integral_constant<int, 0>{}, 0, a0, b0);
+    read_scales(0);
+    using NoMask = std::false_type;
+    int kt = 0;
+    for (; kt + NSTAGE < nk + (kTail ? 0 : 1); kt += NSTAGE) {
+        slice(std::integral_constant<int, 0>{}, kt, NoMask{});
+        slice(std::integral_constant<int, 1>{}, kt + 1, NoMask{});
+        slice(std::integral_constant<int, 2>{}, kt + 2, NoMask{});
+        slice(std::integral_constant<int, 3>{}, kt + 3, NoMask{});
+    }
+    if constexpr (kTail) {  // the last group: 1 to 4 slices, the last possibly cut
+        const int rest = nk - kt;
+        slice(std::integral_constant<int, 0>{}, kt, std::true_type{});
+        if (rest >= 2) slice(std::integral_constant<int, 1>{}, kt + 1, std::true_type{});
+        if (rest >= 3) slice(std::integral_constant<int, 2>{}, kt + 2, std::true_type{});
+        if (rest >= 4) slice(std::integral_constant<int, 3>{}, kt + 3, std::true_type{});
+    }
+    DMA_WAIT_VMCNT(0);  // no copy may still target LDS when the workgroup ends
+
+    // Accumulator layout: register r of lane l is row 8*(r/4) + 4*(l/32) +
+    // r%4, column l%32 of the MFMA tile.  Stores are non-temporal, and with
+    // beta != 0 C is read one MFMA tile ahead of its stores, as in the 16-bit kernel.
+    const int col0 = n0 + wn * (R / 2) + (lane & 31);
+    const int row0 = m0 + wm * (R / 2) + 4 * h;
+    float* cbase = p.C + (int64_t)row0 * p.ldc + col0;
+    const float alpha = p.alpha, beta = p.beta;
+    float bias[TM];
+#pragma unroll
+    for (int tj = 0; tj < TM; ++tj)
+        bias[tj] = p.bias && (!kEdge || col0 + tj * 32 < p.N) ? p.bias[col0 + tj * 32] : -0.0f;
+    auto ok = [&](int ti, int tj, int r) {
+        return !kEdge || (row0 + ti * 32 + 8 * (r >> 2) + (r & 3) < p.M && col0 + tj * 32 < p.N);
+    };
+    auto at = [&](int ti, int tj, int r) -> float* {
+        return &cbase[(int64_t)(ti * 32 + 8 * (r >> 2) + (r & 3)) * p.ldc + tj * 32];
+    };
+#pragma unroll
+    for (int ti = 0; ti < TM; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TM; ++tj) {
+            if (beta == 0.0f) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (ok(ti, tj, r))
+                        __builtin_nontemporal_store(alpha * acc[ti][tj][r] + bias[tj], at(ti, tj, r));
+            } else {
+                float cv[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) cv[r] = ok(ti, tj, r) ? *at(ti, tj, r) : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (ok(ti, tj, r))
+                        __builtin_nontemporal_store(
+                            (alpha * acc[ti][tj][r] + beta * cv[r]) + bias[tj], at(ti, tj, r));
+            }
+        }
+}
+
+template <int R>
+hipError_t launch_tiles(const Params& p, hipStream_t s) {
+    const int tiles_m = (p.M + R - 1) / R, tiles_n = (p.N + R - 1) / R, nb = blocks(p.K);
+    const int64_t wgs = (int64_t)tiles_m * tiles_n;
+    if (wgs > 0x7fffffff) return hipErrorInvalidConfiguration;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, s, p, tiles_m, tiles_n, nb, 0);
+        return hipGetLastError();
+    };
+    if (nb % 16 != 0) return go(mx4_tile_kernel<R, true, true>);
+    if (p.M % R != 0 || p.N % R != 0) return go(mx4_tile_kernel<R, true, false>);
+    return go(mx4_tile_kernel<R, false, false>);
+}
+
+}  // namespace
+
+// Tile size as for the 16-bit kernel.
+hipError_t launch_product_tile(const Params& p, hipStream_t s) {
+    const int64_t t256 = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256);
+    const int64_t t128 = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
+    const double time256 = (double)((t256 + kCUs - 1) / kCUs) * 4.0;
+    const double time128 = (double)((t128 + 2 * kCUs - 1) / (2 * kCUs)) * 2.0 * 1.22;
+    return time128 < time256 ? launch_tiles<128>(p, s) : launch_tiles<256>(p, s);
+}
+
+}  // namespace mx4
+}  // namespace dgt
