@@ -21,7 +21,8 @@ LIBPATH = os.path.join(LIBDIR, "libdgt_gemm.so")
 SOURCES = ["gemm_api.cpp", "k_naive.hip", "k_lds.hip", "k_mfma_f32.hip", "k_mfma_f32_dma.hip",
            "k_mfma_bf16.hip", "k_mfma_bf16_dma.hip", "k_skinny16.hip", "k_skinny_dma.hip",
            "k_skinny_f32.hip",
-           "k_splitk.hip", "mx4_api.cpp", "k_mx4_quant.hip", "k_mx4_tile.hip", "k_mx4_skinny.hip", "orth_api.cpp",
+           "k_splitk.hip", "mx4_api.cpp", "k_mx4_quant.hip", "k_mx4_tile.hip", "k_mx4_skinny.hip",
+           "k_mx4_rows.hip", "orth_api.cpp",
            "k_orth.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

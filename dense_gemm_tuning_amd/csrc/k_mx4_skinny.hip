@@ -1,7 +1,10 @@
-// k_mx4_skinny.hip -- decode-shaped products with a microscaled 4-bit weight:
-// few rows of A (MX4, BF16 or FP16, k contiguous) against B stored N x K.
-// As for the library's other skinny kernels the time is the time to stream
-// B once, here 17 bytes per 32 weights.
+// k_mx4_skinny.hip -- decode-shaped products with a microscaled 4-bit weight
+// of few columns (a share of a layer): few rows of A (MX4, BF16 or FP16, k
+// contiguous) against B stored N x K.  As for the library's other skinny
+// kernels the time is the time to stream B once, here 17 bytes per 32 weights,
+// and with few columns the latency of one pass: narrow strips, K split over
+// the waves.  Wide weights and most batches of more than 16 rows take
+// k_mx4_rows.hip (the choice is made there).
 //
 // Each wave copies its pieces of B straight into a private LDS ring by
 // buffer loads that write LDS (no workgroup barrier in the loop; the scheme of
@@ -20,13 +23,12 @@
 //  * BF16 A: the chunk's 32 values are converted to BF16 with their scale (exact:
 //    4 bits times a power of two) and meet four 16-byte pieces of A in four
 //    16x16x32 products.
-//  * FP16 A: the weights' range does not fit FP16, so A is split into two BF16
-//    parts (11 bits = 8 + 3, exact), once per step, each multiplied with
-//    the converted weights.
-#include <utility>
-
+//  * FP16 A: the scales' range does not fit FP16, so the codes are converted
+//    unscaled and each block's product is scaled as it is added. For that the four
+//    lane groups take the same block, 8 k each (a dword of its codes), and a
+//    row's scale bytes of the whole step are loaded.
 #include "dma_common.hpp"
-#include "mx4.hpp"
+#include "mx4_device.hpp"
 #include "skinny_common.hpp"
 
 namespace dgt {
@@ -39,27 +41,6 @@ using skinny::u32x4_any;
 constexpr int NW = 8;       // waves per workgroup
 constexpr int kBPolicy = 2; // cache policy of the B copies: nt (streamed once)
 
-enum class Kind { MX4, BF16, F16 };
-
-typedef int intx8 __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ intx8 widen(u32x4 x) {
-    return intx8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
-}
-
-// The kernel's body is lambdas over register arrays: one that is not inlined
-// puts them into scratch memory.
-#define INLINE __attribute__((always_inline))
-
-// f(0), .., f(n-1) with compile-time arguments.
-template <int... I, typename F>
-__device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F&& f) {
-    (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-    static_for(std::make_integer_sequence<int, N>{}, f);
-}
-
 // One 16-byte piece per lane into LDS (lane l's bytes at lds + 16*l).
 __device__ __forceinline__ void copy_b(const void* base, uint32_t range, uint8_t* lds,
                                        uint32_t voff) {
@@ -68,35 +49,8 @@ __device__ __forceinline__ void copy_b(const void* base, uint32_t range, uint8_t
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (dma::lds_void*)lds, 16, voff, 0, 0, kBPolicy);
 }
 
-// The 8 values of a dword of codes under scale byte s, as BF16 bits.
-__device__ __forceinline__ u32x4 decode8(uint32_t q, float sc) {
-    return u32x4{
-        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 0)),
-        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 1)),
-        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 2)),
-        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 3))};
-}
-
-// 8 FP16 values as two BF16 parts, x = hi + lo: hi the upper half of x's
-// fp32 form (8 of its 11 bits), lo the rest.  An infinity or NaN is all hi.
-__device__ __forceinline__ void split16(u32x4 x, u32x4& hi, u32x4& lo) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float a = InFmt<In::F16>::widen((uint16_t)(x[e] & 0xffffu));
-        const float b = InFmt<In::F16>::widen((uint16_t)(x[e] >> 16));
-        const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
-        float la = a - __uint_as_float(ha), lb = b - __uint_as_float(hb);
-        la = la == la ? la : 0.0f;
-        lb = lb == lb ? lb : 0.0f;
-        hi[e] = (ha >> 16) | hb;
-        lo[e] = (__float_as_uint(la) >> 16) | (__float_as_uint(lb) & 0xffff0000u);
-    }
-}
-
 // RB: blocks of 16 rows of A.  NG groups of GR stored rows per step.
-// kSingleA: one register buffer of A and scales, reloaded after each step's last
-// products (else two, the next step's loaded one step ahead).
-template <Kind KA, int RB, int ROWB, int NS, int NG, int GR, bool kSingleA>
+template <Kind KA, int RB, int ROWB, int NS, int NG, int GR>
 struct Cfg {
     static constexpr int U = ROWB / 64;            // chunks per lane and step
     static constexpr int STEPB = ROWB / 16;        // blocks per step
@@ -109,15 +63,16 @@ struct Cfg {
     static constexpr int LPR = ROWB / 16;          // lanes per row
     static constexpr int D = NS - 1;               // groups copied ahead
     static constexpr int PA = KA == Kind::MX4 ? 1 : 4;  // 16-byte pieces of A per chunk
+    static constexpr int SW = KA == Kind::F16 ? STEPB / 4 : 1;  // scale dwords per row and step
     static constexpr int LA = RB * U * PA + (KA == Kind::MX4 ? RB : 0) + CB;  // loads per step
     static constexpr int RED_ROWS = STAGE / (COLS * 4) < 16 ? STAGE / (COLS * 4) : 16;
     __device__ static int swz(int r) { return ROWB == 256 ? (r & 15) : ((r >> 1) & 7); }
 };
 
-template <Kind KA, int RB, int ROWB, int NS, int NG, int GR, bool kSingleA>
+template <Kind KA, int RB, int ROWB, int NS, int NG, int GR>
 __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int cols, int nb,
                                                                 int mchunks) {
-    using G = Cfg<KA, RB, ROWB, NS, NG, GR, kSingleA>;
+    using G = Cfg<KA, RB, ROWB, NS, NG, GR>;
     constexpr int U = G::U, D = G::D, STAGE = G::STAGE, PA = G::PA, CB = G::CB;
     static_assert(ROWB == 256 || ROWB == 128, "a row piece is 256 or 128 bytes");
     static_assert(NS == 2 || NS == 4, "ring sizes");
@@ -189,7 +144,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
 
     struct Ops {
         u32x4 a[RB][U * PA];
-        uint32_t sa[RB], sb[CB];  // U scale bytes each
+        uint32_t sa[RB], sb[CB][G::SW];  // U scale bytes each (FP16: the step's)
     };
 
     // Copy group cp of step s into ring stage Q (chunks past the row's end,
@@ -215,8 +170,17 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         s = min(s, nsteps - 1);
         const int b0 = G::STEPB * s + U * g;  // the lane's first block
 #pragma unroll
-        for (int c = 0; c < CB; ++c)
-            o.sb[c] = load_scale(rsb, (uint32_t)((16 * c + i) * p.ldsb + b0));
+        for (int c = 0; c < CB; ++c) {
+            if constexpr (KA == Kind::F16) {
+                static_assert(G::SW == 2, "a step's scales are one 8-byte load");
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(
+                    rsb, (int)((16 * c + i) * p.ldsb + G::STEPB * s), 0, 0);
+                o.sb[c][0] = v[0];
+                o.sb[c][1] = v[1];
+            } else {
+                o.sb[c][0] = load_scale(rsb, (uint32_t)((16 * c + i) * p.ldsb + b0));
+            }
+        }
         if constexpr (KA == Kind::MX4) {
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
@@ -233,13 +197,17 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
             }
         } else {
             const bool cut = kBlock * G::STEPB * (s + 1) > p.K;  // uniform
+            // piece e of the lane: 8 k from here
+            auto at = [&](int e) INLINE {
+                return KA == Kind::F16 ? kBlock * (G::STEPB * s + e) + 8 * g : kBlock * b0 + 8 * e;
+            };
             if (!cut) {
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
                     for (int e = 0; e < U * PA; ++e) {
                         const u32x4_any v = *reinterpret_cast<const u32x4_any*>(
-                            arow[rb] + (int64_t)kBlock * b0 + 8 * e);
+                            arow[rb] + at(e));
                         o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
                     }
             } else {
@@ -248,7 +216,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
 #pragma unroll
                     for (int e = 0; e < U * PA; ++e)
                         o.a[rb][e] = skinny::load16_cached<uint16_t, true, true>(
-                            arow[rb], kBlock * b0 + 8 * e, p.K, true);
+                            arow[rb], at(e), p.K, true);
                 DMA_WAIT_VMCNT(0);
             }
         }
@@ -259,26 +227,50 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         const int left = nb - (G::STEPB * s + U * g);
         const uint32_t keep = left <= 0 ? 0u : left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
 #pragma unroll
-        for (int c = 0; c < CB; ++c) o.sb[c] = (o.sb[c] & keep) | (0x7f7f7f7fu & ~keep);
+        for (int c = 0; c < CB; ++c) {
+            if constexpr (KA == Kind::F16) {
+#pragma unroll
+                for (int d = 0; d < G::SW; ++d) {
+                    const int n = nb - (G::STEPB * s + 4 * d);
+                    const uint32_t k = n <= 0 ? 0u : n >= 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
+                    o.sb[c][d] = (o.sb[c][d] & k) | (0x7f7f7f7fu & ~k);
+                }
+            } else {
+                o.sb[c][0] = (o.sb[c][0] & keep) | (0x7f7f7f7fu & ~keep);
+            }
+        }
         if constexpr (KA == Kind::MX4) {
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) o.sa[rb] = (o.sa[rb] & keep) | (0x7f7f7f7fu & ~keep);
         }
     };
-    u32x4 ahi[KA == Kind::F16 ? RB : 1][KA == Kind::F16 ? U * PA : 1];
-    u32x4 alo[KA == Kind::F16 ? RB : 1][KA == Kind::F16 ? U * PA : 1];
-    auto prepare = [&](int s, Ops& o) INLINE {
-        mask_scales(s, o);
-        if constexpr (KA == Kind::F16) {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-                for (int e = 0; e < U * PA; ++e) split16(o.a[rb][e], ahi[rb][e], alo[rb][e]);
-        }
-    };
     auto compute = [&](auto qc, auto cpc, const Ops& o) INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         const uint8_t* st = dma::pick<Q>(st0, st1, st2, st3) + STAGE * wave;
+        if constexpr (KA == Kind::F16) {
+            uint32_t w[G::NBK][G::STEPB];
+#pragma unroll
+            for (int b = 0; b < G::NBK; ++b)
+#pragma unroll
+                for (int e = 0; e < G::STEPB; ++e)
+                    w[b][e] = *reinterpret_cast<const uint32_t*>(
+                        st + (16 * b + i) * ROWB + ((e ^ G::swz(16 * b + i)) << 4) + 4 * g);
+            __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead of the products
+#pragma unroll
+            for (int b = 0; b < G::NBK; ++b)
+#pragma unroll
+                for (int e = 0; e < G::STEPB; ++e) {
+                    const u32x4 v = decode8_f16(w[b][e]);
+                    const float sc = scale_number(o.sb[G::NBK * cp + b][e / 4], e % 4);
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb)
+                        acc[rb][G::NBK * cp + b] =
+                            scaled_product_f16(o.a[rb][e], v, sc, acc[rb][G::NBK * cp + b]);
+                    // four products at a time: all at once do not fit the registers
+                    if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                }
+            return;
+        }
         u32x4 bop[G::NBK][U];
 #pragma unroll
         for (int b = 0; b < G::NBK; ++b)
@@ -296,20 +288,15 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
                     for (int rb = 0; rb < RB; ++rb)
                         acc[rb][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                             widen(o.a[rb][u]), widen(bop[b][u]), acc[rb][c], 4, 4, u, (int)o.sa[rb],
-                            u, (int)o.sb[c]);
+                            u, (int)o.sb[c][0]);
                 } else {
-                    const float sc = scale_bits((o.sb[c] >> (8 * u)) & 255u);
+                    const float sc = scale_bits((o.sb[c][0] >> (8 * u)) & 255u);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const u32x4 w = decode8(bop[b][u][j], sc);
 #pragma unroll
                         for (int rb = 0; rb < RB; ++rb) {
-                            if constexpr (KA == Kind::F16) {
-                                acc[rb][c] = mfma16x16x32<In::BF16>(ahi[rb][4 * u + j], w, acc[rb][c]);
-                                acc[rb][c] = mfma16x16x32<In::BF16>(alo[rb][4 * u + j], w, acc[rb][c]);
-                            } else {
-                                acc[rb][c] = mfma16x16x32<In::BF16>(o.a[rb][4 * u + j], w, acc[rb][c]);
-                            }
+                            acc[rb][c] = mfma16x16x32<In::BF16>(o.a[rb][4 * u + j], w, acc[rb][c]);
                         }
                     }
                 }
@@ -322,17 +309,13 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
     };
 
     // Group cp of step s, in ring stage Q.  The wave first copies the group D
-    // places ahead, then waits until its own copy of this group has landed:
-    // newer are the D groups' copies after it, and this step's load of
-    // operands where that came after the copy.
-    //  * Two operand buffers: the next step's operands are loaded in this step's
-    //    cp = 0 phase after its copy: newer than this group's copy when
-    //    that was issued in this phase or before (cp <= D).
-    //  * One buffer: this step's operands were loaded at the end of the
-    //    previous step: newer when the copy was issued before that (cp < D).
-    // Loads of earlier steps may be newer too; not counting them only waits for
-    // more.  A load that waited for everything (a cut-off step) leaves no older
-    // copy in flight, so the counts hold after it as well.
+    // places ahead (in phase 0 it then loads the next step's operands), then waits until its
+    // own copy of this group has landed: newer are the D groups' copies after
+    // it, and this step's load of operands when that group's copy was issued in this
+    // step's phase 0 or before (cp <= D).  Loads of earlier steps may be newer
+    // too; not counting them only waits for more.  A load that waited for
+    // everything (a cut-off step) leaves no older copy in flight, so the
+    // counts hold after it as well.
     auto phase = [&](auto qc, auto cpc, int s, Ops& o, Ops& next) INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         constexpr int ahead = cp + D;
@@ -340,21 +323,16 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         issue(std::integral_constant<int, (Q + D) % NS>{}, std::integral_constant<int, ahead % NG>{},
               s + ahead / NG);
         fence();
-        if constexpr (!kSingleA && cp == 0) {
+        if constexpr (cp == 0) {
             load_ops(s + 1, next);
             fence();
         }
-        constexpr bool newer = kSingleA ? cp < D : cp <= D;
-        constexpr int after = G::INSTR * D + (newer ? G::LA : 0);
+        constexpr int after = G::INSTR * D + (cp <= D ? G::LA : 0);
         DMA_WAIT_VMCNT((after < 63 ? after : 63));
         fence();
-        if constexpr (cp == 0) prepare(s, o);
+        if constexpr (cp == 0) mask_scales(s, o);
         compute(qc, cpc, o);
         fence();
-        if constexpr (kSingleA && cp == NG - 1) {
-            load_ops(s + 1, next);
-            fence();
-        }
     };
     // Steps whose groups start at ring stage Q0.
     auto step = [&](auto q0c, int s, Ops& o, Ops& next) INLINE {
@@ -373,25 +351,18 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
             });
             fence();
         };
-        if constexpr (kSingleA) {
-            copies();
-            load_ops(s0, o0);
-            fence();
-        } else {
-            load_ops(s0, o0);
-            fence();
-            copies();
-        }
+        load_ops(s0, o0);
+        fence();
+        copies();
         // Unrolled so that ring stages and operand buffers are compile-time.
         constexpr int kRing = NS > NG ? NS / NG : 1;
-        constexpr int kUnroll = kSingleA ? kRing : (kRing > 2 ? kRing : 2);
+        constexpr int kUnroll = kRing > 2 ? kRing : 2;
         for (int s = s0; s < s1; s += kUnroll) {
             static_for<kUnroll>([&](auto jc) INLINE {
                 constexpr int j = decltype(jc)::value;
                 if (s + j >= s1) return;
                 using Q0 = std::integral_constant<int, (j * NG) % NS>;
-                if constexpr (kSingleA) step(Q0{}, s + j, o0, o0);
-                else if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1);
+                if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1);
                 else step(Q0{}, s + j, o1, o0);
             });
         }
@@ -431,45 +402,42 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         }
 }
 
-template <Kind KA, int RB, int ROWB, int NS, int NG, int GR, bool kSingleA>
-hipError_t launch_cfg(const Params& p, int cols, hipStream_t s) {
+template <Kind KA, int RB, int ROWB, int NS, int NG, int GR>
+hipError_t launch_cfg(const Params& p, hipStream_t s) {
+    constexpr int cols = NG * GR;
     const int mchunks = (p.M + 16 * RB - 1) / (16 * RB);
     const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
     const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
     if (wgs > 0x7fffffff || 8 * (int64_t)mchunks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((mx4_skinny_kernel<KA, RB, ROWB, NS, NG, GR, kSingleA>), dim3((unsigned)wgs),
+    hipLaunchKernelGGL((mx4_skinny_kernel<KA, RB, ROWB, NS, NG, GR>), dim3((unsigned)wgs),
                        dim3(NW * 64), 0, s, p, cols, blocks(p.K), mchunks);
     return hipGetLastError();
 }
 
-// Strip width: the widest whose workgroups still fill the CUs.
-template <Kind KA, int RB, int ROWB, int NS, bool kSingleA>
-hipError_t launch_rows(const Params& p, hipStream_t s) {
-    constexpr int64_t kFill = 200;
+// Strip width: the narrowest whose workgroups take one round of the CUs.  At
+// K = 8192, MX4, M = 8, us for 16 / 32 / 64 columns: N = 3584 7.3 / 8.9 / 12.4,
+// 8192 12.0 / 10.9 / 13.5, 14336 20.4 / 18.7 / 16.3.
+template <Kind KA, int RB, int ROWB, int NS>
+hipError_t launch_strip(const Params& p, hipStream_t s) {
     const int64_t chunks = (p.M + 16 * RB - 1) / (16 * RB);
-    auto wgs = [&](int cols) { return ((int64_t)p.N + cols - 1) / cols * chunks; };
-    if (wgs(112) >= 256) return launch_cfg<KA, RB, ROWB, NS, 4, 32, kSingleA>(p, wgs(128) >= 256 ? 128 : 112, s);
-    if (wgs(64) >= kFill) return launch_cfg<KA, RB, ROWB, NS, 2, 32, kSingleA>(p, 64, s);
-    if (wgs(32) >= kFill) return launch_cfg<KA, RB, ROWB, NS, 1, 32, kSingleA>(p, 32, s);
-    return launch_cfg<KA, RB, ROWB, NS, 1, 16, kSingleA>(p, 16, s);
+    auto fits = [&](int cols) { return ((int64_t)p.N + cols - 1) / cols * chunks <= dma::kCUs; };
+    if (fits(16)) return launch_cfg<KA, RB, ROWB, NS, 1, 16>(p, s);
+    if (fits(32)) return launch_cfg<KA, RB, ROWB, NS, 1, 32>(p, s);
+    return launch_cfg<KA, RB, ROWB, NS, 2, 32>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_product(const Params& p, hipStream_t s) {
-    switch ((p.M + 15) / 16) {
-        case 1: return launch_rows<Kind::MX4, 1, 256, 2, false>(p, s);
-        case 2: return launch_rows<Kind::MX4, 2, 256, 2, false>(p, s);
-        case 3: return launch_rows<Kind::MX4, 3, 128, 4, true>(p, s);
-        case 4: return launch_rows<Kind::MX4, 4, 128, 4, true>(p, s);
-        default: return hipErrorInvalidConfiguration;
-    }
+// M <= 32.
+hipError_t launch_skinny(const Params& p, hipStream_t s) {
+    return p.M <= 16 ? launch_strip<Kind::MX4, 1, 256, 2>(p, s)
+                     : launch_strip<Kind::MX4, 2, 256, 2>(p, s);
 }
 
-hipError_t launch_product16(In t, const Params& p, hipStream_t s) {
-    if (t == In::F16) return launch_rows<Kind::F16, 1, 128, 4, false>(p, s);
-    return p.M <= 16 ? launch_rows<Kind::BF16, 1, 256, 2, false>(p, s)
-                     : launch_rows<Kind::BF16, 2, 128, 4, false>(p, s);
+hipError_t launch_skinny16(In t, const Params& p, hipStream_t s) {
+    if (t == In::F16) return launch_strip<Kind::F16, 1, 128, 4>(p, s);
+    return p.M <= 16 ? launch_strip<Kind::BF16, 1, 256, 2>(p, s)
+                     : launch_strip<Kind::BF16, 2, 128, 4>(p, s);
 }
 
 }  // namespace mx4

@@ -162,10 +162,16 @@ def small_ints(rng, rows, K):
     return rng.integers(-3, 4, (rows, K)).astype(np.float64)
 
 
+# Weights of enough columns for strips of 64 and 128 on every compute unit, a
+# last strip of one column, K tails of one element, one block and many steps.
+WIDE = [(1, 14337, 33), (8, 16400, 160), (16, 28673, 97), (20, 9000, 544), (32, 16500, 300), (40, 17000, 1056),
+        (64, 33000, 130), (100, 9000, 320)]
+
+
 # Bit-exact: MX4 operands are multiples of 1/4 of at most 24, so products are
 # multiples of 1/16 of at most 576 and every partial sum is below 576 K * 16 <
 # 2^24 units for K <= 1820; beyond that the operands' scales are 2^-1 .. 2^0.
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + WIDE)
 @pytest.mark.parametrize("kind", ["mx4", "bf16", "f16"])
 def test_product_exact_values(M, N, K, kind):
     say("product", M, N, K, kind)
