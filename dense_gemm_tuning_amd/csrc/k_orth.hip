@@ -3,8 +3,13 @@
 //     X <- G / (|G|_F + eps);   steps times:  S = X X^T,  X <- a X + (b S + c S S) X
 //
 // (M <= N; for M > N the same from the right: S = X^T X, X <- a X + X (b S + c S S),
-// so no matrix is transposed in memory).  The three products of a step run on
-// the library's FP16 tile kernels with fp32 sums.
+// so no matrix is transposed in memory).  The three products of a step are the
+// library's FP16 tile product (mfma16_tile.hpp) with epilogues of their own:
+//   S   its tiles on and below the diagonal (half the work), each stored and mirrored;
+//   B = b S + c S S   likewise, S's rows serving as its columns;
+//   X   a X added from the two halves below, the next two halves or the bf16 result
+//       stored.
+// A Gram matrix with too few tiles for the chip is summed over k in parts.
 //
 // Rounding.  The products' operands are FP16.  Each step multiplies what
 // rounding X adds in the weak singular directions by up to a (3.4 with the
@@ -22,6 +27,7 @@
 // range moves.
 #include <cmath>
 
+#include "mfma16_tile.hpp"
 #include "orth.hpp"
 
 namespace dgt {
@@ -29,26 +35,57 @@ namespace orth {
 
 namespace {
 
-constexpr int NT = 256;
+using namespace mfma16;
+
 constexpr float kGramScale = 4096.0f;  // 2^12
 constexpr float kPolyScale = 1024.0f;  // 2^10
 
+typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
+
 int scale_exp(const Plan& p) {  // round(log2(sqrt(max(M, N))))
-    return (int)std::lround(0.5 * std::log2((double)(p.M > p.N ? p.M : p.N)));
+    return (int)std::lround(0.5 * std::log2((double)p.k));
 }
 
-// kNormParts partial sums of squares per matrix, in 64 bits: workgroup x of
-// matrix blockIdx.y sums elements x*NT + t, + kNormParts*NT, ...
+// Eight elements of a row, widened; `vec`: the row starts and pitch are on 16
+// bytes.
+template <In T>
+__device__ __forceinline__ void load8(const typename InFmt<T>::S* row, int col, int N, bool vec,
+                                      float (&v)[8]) {
+    using E = typename InFmt<T>::S;
+    if (vec && col + 8 <= N) {
+        constexpr int W = 16 / sizeof(E);  // elements per 16 bytes
+#pragma unroll
+        for (int h = 0; h < 8 / W; ++h) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(row + col + W * h);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if constexpr (T == In::F32) v[W * h + e] = __uint_as_float(x[e]);
+                else v[e] = InFmt<T>::widen((uint16_t)(x[e / 2] >> (16 * (e % 2))));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = col + e < N ? load_in<T>(row + col + e) : 0.0f;
+    }
+}
+
+// kNormParts partial sums of squares per matrix, in 64 bits (an fp32 input's
+// squares leave fp32's range): workgroup x of matrix blockIdx.y takes every
+// kNormParts-th run of 8 * NT elements.  The order is fixed.
 template <In T>
 __global__ __launch_bounds__(NT) void norm_kernel(const typename InFmt<T>::S* G, int64_t ldg,
-                                                  int64_t stride, int M, int N, double* parts) {
+                                                  int64_t stride, int M, int N, bool vec,
+                                                  double* parts) {
     G += blockIdx.y * stride;
-    const int64_t total = (int64_t)M * N;
+    const int per_row = (N + 7) / 8;
+    const int64_t total = (int64_t)M * per_row;
     double sum = 0.0;
     for (int64_t e = (int64_t)blockIdx.x * NT + threadIdx.x; e < total;
          e += (int64_t)kNormParts * NT) {
-        const double v = load_in<T>(G + e / N * ldg + e % N);
-        sum += v * v;
+        float v[8];
+        load8<T>(G + e / per_row * ldg, (int)(e % per_row) * 8, N, vec, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += (double)v[i] * (double)v[i];
     }
     __shared__ double red[NT];
     red[threadIdx.x] = sum;
@@ -60,168 +97,445 @@ __global__ __launch_bounds__(NT) void norm_kernel(const typename InFmt<T>::S* G,
     if (threadIdx.x == 0) parts[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = red[0];
 }
 
-struct Halves {
-    _Float16 hi, lo;
-};
-__device__ __forceinline__ Halves split(float x) {
-    Halves h;
-    h.hi = (_Float16)x;
-    h.lo = (_Float16)(x - (float)h.hi);
-    return h;
+// Eight values as two FP16 halves, x = hi + lo to 22 bits.
+__device__ __forceinline__ void split8(const float (&x)[8], halfx8& hi, halfx8& lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        hi[e] = (_Float16)x[e];
+        lo[e] = (_Float16)(x[e] - (float)hi[e]);
+    }
 }
 
 // X <- G * 2^x_exp / (|G| + eps) as two halves; zeros in the padding columns.
 template <In T>
 __global__ __launch_bounds__(NT) void init_kernel(const typename InFmt<T>::S* G, int64_t ldg,
-                                                  int64_t stride, int M, int N, const double* parts,
-                                                  double eps, double scale, _Float16* hi,
-                                                  _Float16* lo, int64_t ldx) {
+                                                  int64_t stride, int M, int N, bool vec,
+                                                  const double* parts, double eps, double scale,
+                                                  _Float16* hi, _Float16* lo, int64_t ldx) {
+    static_assert(kNormParts == NT, "one partial sum per lane");
     const int64_t z = blockIdx.y;
     G += z * stride;
     hi += z * M * ldx;
     lo += z * M * ldx;
-    double sum = 0.0;
-    for (int i = 0; i < kNormParts; ++i) sum += parts[z * kNormParts + i];
-    const double inv = scale / (sqrt(sum) + eps);
-    const int64_t total = (int64_t)M * ldx;
+    __shared__ double red[NT];
+    red[threadIdx.x] = parts[z * kNormParts + threadIdx.x];
+    __syncthreads();
+    for (int h = NT / 2; h > 0; h /= 2) {
+        if ((int)threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
+        __syncthreads();
+    }
+    const double inv = scale / (sqrt(red[0]) + eps);
+    const int per_row = (int)(ldx / 8);
+    const int64_t total = (int64_t)M * per_row;
     for (int64_t e = (int64_t)blockIdx.x * NT + threadIdx.x; e < total;
          e += (int64_t)gridDim.x * NT) {
-        const int64_t row = e / ldx;
-        const int col = (int)(e % ldx);
-        const Halves h =
-            split(col < N ? (float)((double)load_in<T>(G + row * ldg + col) * inv) : 0.0f);
-        hi[e] = h.hi;
-        lo[e] = h.lo;
+        const int64_t row = e / per_row;
+        const int col = (int)(e % per_row) * 8;
+        float v[8];
+        load8<T>(G + row * ldg, col, N, vec, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = col + i < N ? (float)((double)v[i] * inv) : 0.0f;
+        halfx8 h, l;
+        split8(v, h, l);
+        *reinterpret_cast<halfx8*>(hi + row * ldx + col) = h;
+        *reinterpret_cast<halfx8*>(lo + row * ldx + col) = l;
     }
 }
 
-// S <- the Gram matrix's sums times f, in FP16.
-__global__ __launch_bounds__(NT) void gram_kernel(const float* C, _Float16* S, int64_t total,
-                                                  float f) {
-    for (int64_t e = (int64_t)blockIdx.x * NT + threadIdx.x; e < total;
-         e += (int64_t)gridDim.x * NT)
-        S[e] = (_Float16)(C[e] * f);
-}
+// ------------------------------------------------------------- epilogues
+//
+// Accumulators reach memory through the wavefront's LDS region, one row of
+// MFMA tiles (32 x R/2 fp32) at a time, so that a lane handles 8 neighbouring
+// columns (or, mirrored, 8 neighbouring rows) with 16-byte accesses.  Column c of
+// row r sits at c ^ 32*(r/4 & 1): the two half-waves of an accumulator write rows 4
+// apart, which then differ in banks.
 
-// B <- fb * S + fc * (sums of S*S), in FP16.
-__global__ __launch_bounds__(NT) void poly_kernel(const float* C, const _Float16* S, _Float16* B,
-                                                  int64_t total, float fb, float fc) {
-    for (int64_t e = (int64_t)blockIdx.x * NT + threadIdx.x; e < total;
-         e += (int64_t)gridDim.x * NT)
-        B[e] = (_Float16)(fb * (float)S[e] + fc * C[e]);
-}
-
-// X' <- a * (hi + lo) + f * sums: two halves, or the result (times out_scale)
-// in bf16.
-template <bool kLast>
-__global__ __launch_bounds__(NT) void update_kernel(const float* C, const _Float16* hi,
-                                                    const _Float16* lo, int M, int N, int64_t ldx,
-                                                    float a, float f, _Float16* hi2, _Float16* lo2,
-                                                    uint16_t* O, int64_t ldo, int64_t stride_o,
-                                                    float out_scale) {
-    const int64_t z = blockIdx.y, base = z * M * ldx;
-    const int64_t total = (int64_t)M * ldx;
-    for (int64_t e = (int64_t)blockIdx.x * NT + threadIdx.x; e < total;
-         e += (int64_t)gridDim.x * NT) {
-        const int64_t row = e / ldx;
-        const int col = (int)(e % ldx);
-        const float x = a * ((float)hi[base + e] + (float)lo[base + e]) + f * C[base + e];
-        if constexpr (kLast) {
-            if (col < N)
-                O[z * stride_o + row * ldo + col] =
-                    __builtin_bit_cast(uint16_t, (__bf16)(x * out_scale));
-        } else {
-            const Halves h = split(col < N ? x : 0.0f);
-            hi2[base + e] = h.hi;
-            lo2[base + e] = h.lo;
+template <int R>
+struct Chunk {
+    static constexpr int W = R / 2;           // columns
+    static constexpr int GROUPS = W / 8;      // column groups of 8
+    float* mem;
+    __device__ static int at(int r, int c) { return r * W + (c ^ (32 * ((r >> 2) & 1))); }
+    // Lanes read what other lanes of the wavefront wrote: LDS keeps their
+    // order, the compiler has to as well.
+    __device__ static void fence() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    // MFMA tiles of tile row ti.
+    __device__ void put(const floatx16 (&acc)[Geo<R>::TM], int lane) const {
+        const int h = lane >> 5;
+        fence();
+#pragma unroll
+        for (int tj = 0; tj < Geo<R>::TM; ++tj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                mem[at(8 * (r >> 2) + 4 * h + (r & 3), tj * 32 + (lane & 31))] = acc[tj][r];
+        fence();
+    }
+    __device__ void row8(int r, int c, float (&v)[8]) const {
+        const floatx4 a = *reinterpret_cast<const floatx4*>(mem + at(r, c));
+        const floatx4 b = *reinterpret_cast<const floatx4*>(mem + at(r, c + 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    }
+    __device__ void col8(int r, int c, float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = mem[at(r + e, c)];
+    }
+    // fn(row, column, 8 values along the row) over the chunk, or with
+    // kMirror fn(column, row, 8 values down the column).
+    template <bool kMirror, typename Fn>
+    __device__ void each(int lane, Fn&& fn) const {
+#pragma unroll
+        for (int i = 0; i < 32 * W / 8 / 64; ++i) {
+            const int e = 64 * i + lane;
+            float v[8];
+            if constexpr (kMirror) {
+                const int c = e % W, r = e / W * 8;
+                col8(r, c, v);
+                fn(c, r, v);
+            } else {
+                const int r = e / GROUPS, c = e % GROUPS * 8;
+                row8(r, c, v);
+                fn(r, c, v);
+            }
         }
     }
+};
+
+// Tiles on and below the diagonal, numbered row by row; XCD x takes a
+// contiguous range of the launch's tiles.
+__device__ __forceinline__ TileIdx lower_tile(int64_t per_problem) {
+    const int64_t total = per_problem * gridDim.y;
+    const int64_t lin = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    const int64_t x = lin % kXcds, q = lin / kXcds, per = total / kXcds, rem = total % kXcds;
+    const int64_t g = x < rem ? x * (per + 1) + q : rem * (per + 1) + (x - rem) * per + q;
+    const int64_t idx = g % per_problem;
+    int bm = (int)((sqrt(8.0 * (double)idx + 1.0) - 1.0) * 0.5);
+    while ((int64_t)bm * (bm + 1) / 2 > idx) --bm;  // the root may be off by its rounding
+    while ((int64_t)(bm + 1) * (bm + 2) / 2 <= idx) ++bm;
+    return TileIdx{(int)(g / per_problem), bm, (int)(idx - (int64_t)bm * (bm + 1) / 2)};
+}
+
+// A symmetric n x n product's tile: OUT <- f1 * sums (+ f2 * D), and mirrored
+// off the diagonal; D is OUT's layout.
+template <int R, bool TA, bool TB, bool kEdge, bool kTail, bool kAdd>
+__global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void symmetric_kernel(
+    GemmParams p, int64_t tiles, _Float16* out, const _Float16* add, int64_t ld, int64_t size,
+    float f1, float f2) {
+    const TileIdx tile = lower_tile(tiles);
+    select_problem(p, tile.z);
+    out += tile.z * size;
+    if constexpr (kAdd) add += tile.z * size;
+    const int m0 = tile.bm * R, n0 = tile.bn * R;
+    dma_tile<In::F16, R, TA, TB, kEdge, kTail>(
+        p, m0, n0, nullptr, [&](const auto& acc, int wm, int wn, int lane, uint8_t* mem) {
+            const Chunk<R> chunk{reinterpret_cast<float*>(mem)};
+            static_assert(32 * Chunk<R>::W * 4 <= (TA ? Geo<R>::MN_STAGE : Geo<R>::KC_STAGE / 2), "");
+#pragma unroll
+            for (int ti = 0; ti < Geo<R>::TM; ++ti) {
+                const int row0 = m0 + wm * (R / 2) + ti * 32, col0 = n0 + wn * (R / 2);
+                chunk.put(acc[ti], lane);
+                chunk.template each<false>(lane, [&](int r, int c, const float (&v)[8]) {
+                    const int row = row0 + r, col = col0 + c;
+                    if (kEdge && (row >= p.M || col >= p.N)) return;
+                    halfx8 o;
+                    if constexpr (kAdd) {
+                        const halfx8 d = *reinterpret_cast<const halfx8*>(add + row * ld + col);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = (_Float16)(f2 * (float)d[e] + f1 * v[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = (_Float16)(f1 * v[e]);
+                    }
+                    *reinterpret_cast<halfx8*>(out + row * ld + col) = o;
+                });
+                if (m0 != n0)  // D is symmetric too: its mirrored rows are read
+                    chunk.template each<true>(lane, [&](int c, int r, const float (&v)[8]) {
+                        const int row = col0 + c, col = row0 + r;
+                        if (kEdge && (row >= p.N || col >= p.M)) return;
+                        halfx8 o;
+                        if constexpr (kAdd) {
+                            const halfx8 d = *reinterpret_cast<const halfx8*>(add + row * ld + col);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = (_Float16)(f2 * (float)d[e] + f1 * v[e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = (_Float16)(f1 * v[e]);
+                        }
+                        *reinterpret_cast<halfx8*>(out + row * ld + col) = o;
+                    });
+            }
+        });
+}
+
+// X' = a (hi + lo) + f * sums: two halves, or (kLast) the result in bf16.
+struct Update {
+    const _Float16 *hi, *lo;
+    _Float16 *hi2, *lo2;
+    int64_t ldx, x_size;
+    float a, f;
+    uint16_t* O;
+    int64_t ldo, stride_o;
+    float out_scale;
+    bool o_vec;  // O's rows on 16 bytes
+};
+template <int R, bool TB, bool kEdge, bool kTail, bool kLast>
+__global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams p, int tiles_m,
+                                                                    int tiles_n, Update u) {
+    const TileIdx tile = xcd_tile(tiles_m, tiles_n, true);
+    select_problem(p, tile.z);
+    const int m0 = tile.bm * R, n0 = tile.bn * R;
+    const int64_t xz = tile.z * u.x_size;
+    uint16_t* O = u.O + tile.z * u.stride_o;
+    dma_tile<In::F16, R, false, TB, kEdge, kTail>(
+        p, m0, n0, nullptr, [&](const auto& acc, int wm, int wn, int lane, uint8_t* mem) {
+            const Chunk<R> chunk{reinterpret_cast<float*>(mem)};
+#pragma unroll
+            for (int ti = 0; ti < Geo<R>::TM; ++ti) {
+                const int row0 = m0 + wm * (R / 2) + ti * 32, col0 = n0 + wn * (R / 2);
+                chunk.put(acc[ti], lane);
+                chunk.template each<false>(lane, [&](int r, int c, const float (&v)[8]) {
+                    const int row = row0 + r, col = col0 + c;
+                    if (kEdge && (row >= p.M || col >= p.N)) return;
+                    const int64_t at = xz + (int64_t)row * u.ldx + col;
+                    const halfx8 h = *reinterpret_cast<const halfx8*>(u.hi + at);
+                    const halfx8 l = *reinterpret_cast<const halfx8*>(u.lo + at);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = u.a * ((float)h[e] + (float)l[e]) + u.f * v[e];
+                    if constexpr (kLast) {
+                        bf16x8 o;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = (__bf16)(x[e] * u.out_scale);
+                        uint16_t* out = O + (int64_t)row * u.ldo + col;
+                        if (u.o_vec && col + 8 <= p.N) {
+                            *reinterpret_cast<bf16x8*>(out) = o;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const __bf16 b = o[e];
+                                if (col + e < p.N) out[e] = __builtin_bit_cast(uint16_t, b);
+                            }
+                        }
+                    } else {
+                        halfx8 nh, nl;
+                        split8(x, nh, nl);
+                        *reinterpret_cast<halfx8*>(u.hi2 + at) = nh;
+                        *reinterpret_cast<halfx8*>(u.lo2 + at) = nl;
+                    }
+                });
+            }
+        });
+}
+
+// One part of the Gram matrix's sums: tile blockIdx.x, part blockIdx.y of
+// problem blockIdx.z, kGramTile^2 floats to its place in `partial`.
+template <bool TA, bool TB, bool kTail>
+__global__ __launch_bounds__(NT, 2) void gram_part_kernel(GemmParams p, int kc, int splits,
+                                                          float* partial) {
+    constexpr int R = kGramTile;
+    const int idx = blockIdx.x, part = blockIdx.y;
+    int bm = 0;
+    while ((bm + 1) * (bm + 2) / 2 <= idx) ++bm;
+    const int bn = idx - bm * (bm + 1) / 2;
+    select_problem(p, blockIdx.z);
+    const int k0 = part * kc;
+    const int64_t skip = TA ? (int64_t)k0 * p.lda : k0;
+    p.A = static_cast<const uint16_t*>(p.A) + skip;
+    p.B = static_cast<const uint16_t*>(p.B) + skip;
+    p.K = min(kc, p.K - k0);
+    float* raw = partial + (((int64_t)blockIdx.z * gridDim.x + idx) * splits + part) * R * R;
+    dma_tile<In::F16, R, TA, TB, true, kTail>(p, bm * R, bn * R, raw);
+}
+
+// S <- f * the parts' sums, in part order, stored and mirrored.  Each lane
+// takes 8 neighbouring elements of a tile's row; a workgroup 16 rows.
+__global__ __launch_bounds__(NT) void gram_join_kernel(const float* partial, int splits, int n,
+                                                       _Float16* S, int64_t ld, int64_t size,
+                                                       float f) {
+    constexpr int R = kGramTile;
+    __shared__ _Float16 turn[16][R + 2];
+    const int idx = blockIdx.x, strip = blockIdx.y;
+    int bm = 0;
+    while ((bm + 1) * (bm + 2) / 2 <= idx) ++bm;
+    const int bn = idx - bm * (bm + 1) / 2;
+    S += blockIdx.z * size;
+    partial += ((int64_t)blockIdx.z * gridDim.x + idx) * splits * R * R;
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 8;
+    const float* src = partial + (16 * strip + r) * R + c;
+    floatx4 s0 = *reinterpret_cast<const floatx4*>(src);
+    floatx4 s1 = *reinterpret_cast<const floatx4*>(src + 4);
+    for (int i = 1; i < splits; ++i) {
+        s0 += *reinterpret_cast<const floatx4*>(src + (int64_t)i * R * R);
+        s1 += *reinterpret_cast<const floatx4*>(src + (int64_t)i * R * R + 4);
+    }
+    halfx8 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        o[e] = (_Float16)(f * s0[e]);
+        o[4 + e] = (_Float16)(f * s1[e]);
+    }
+    const int row0 = bm * R + 16 * strip, col0 = bn * R;
+    if (row0 + r < n && col0 + c < n)
+        *reinterpret_cast<halfx8*>(S + (row0 + r) * ld + col0 + c) = o;
+    if (bm == bn) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turn[r][c + e] = o[e];
+    __syncthreads();
+    const int col = threadIdx.x / 2, half = threadIdx.x % 2 * 8;  // column of the tile, 8 rows
+    halfx8 t;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = turn[half + e][col];
+    if (col0 + col < n && row0 + half < n)
+        *reinterpret_cast<halfx8*>(S + (col0 + col) * ld + row0 + half) = t;
 }
 
 unsigned grid_for(int64_t items) {
     const int64_t g = (items + NT - 1) / NT;
-    return (unsigned)(g < 16384 ? g : 16384);  // grid-stride loops cover the rest
+    return (unsigned)(g < 2048 ? g : 2048);  // grid-stride loops cover the rest
 }
 
-// C <- op(A) op(B), FP16 operands of a batch.
-hipError_t product(const Plan& p, int M, int N, int K, const void* A, int64_t lda, int64_t sa,
-                   int ta, const void* B, int64_t ldb, int64_t sb, int tb, float* C, int64_t ldc,
-                   int64_t sc, hipStream_t s) {
+GemmParams operands(const Plan& p, int M, int N, int K, const _Float16* A, int64_t lda, int64_t sa,
+                    const _Float16* B, int64_t ldb, int64_t sb) {
     GemmParams g = {};
     g.M = M; g.N = N; g.K = K;
-    g.alpha = 1.0f;
-    g.A = A; g.lda = lda; g.stride_a = sa * 2; g.ta = ta;
-    g.B = B; g.ldb = ldb; g.stride_b = sb * 2; g.tb = tb;
-    g.C = C; g.ldc = ldc; g.stride_c = sc;
+    g.A = A; g.lda = lda; g.stride_a = sa * 2;
+    g.B = B; g.ldb = ldb; g.stride_b = sb * 2;
     g.batch = p.batch;
-    return launch_mfma16<In::F16>(g, s);
+    return g;
+}
+
+// The tile size with less time by the wave model of the 16-bit kernel (t256,
+// t128: tiles of the launch).
+bool use128(int64_t t256, int64_t t128) {
+    const double time256 = (double)((t256 + kCUs - 1) / kCUs) * 4.0;
+    const double time128 = (double)((t128 + 2 * kCUs - 1) / (2 * kCUs)) * 2.0 * 1.22;
+    return time128 < time256;
+}
+
+template <bool TA, bool TB, bool kAdd>
+hipError_t symmetric(const GemmParams& g, _Float16* out, const _Float16* add, int64_t ld,
+                     int64_t size, float f1, float f2, hipStream_t s) {
+    auto go = [&](auto rc) {
+        constexpr int R = decltype(rc)::value;
+        const int64_t tiles = lower_tiles(g.M, R);
+        if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+        auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)tiles, g.batch), dim3(NT), 0, s, g, tiles,
+                               out, add, ld, size, f1, f2);
+            return hipGetLastError();
+        };
+        if (g.K % (BK * NSTAGE) != 0) return launch(symmetric_kernel<R, TA, TB, true, true, kAdd>);
+        if (g.M % R != 0) return launch(symmetric_kernel<R, TA, TB, true, false, kAdd>);
+        return launch(symmetric_kernel<R, TA, TB, false, false, kAdd>);
+    };
+    return use128(lower_tiles(g.M, 256) * g.batch, lower_tiles(g.M, 128) * g.batch)
+               ? go(std::integral_constant<int, 128>{})
+               : go(std::integral_constant<int, 256>{});
+}
+
+template <bool TB>
+hipError_t update(const GemmParams& g, const Update& u, bool last, hipStream_t s) {
+    auto go = [&](auto rc, auto lc) {
+        constexpr int R = decltype(rc)::value;
+        constexpr bool kLast = decltype(lc)::value;
+        const int tm = (g.M + R - 1) / R, tn = (g.N + R - 1) / R;
+        const int64_t tiles = (int64_t)tm * tn;
+        if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+        auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)tiles, g.batch), dim3(NT), 0, s, g, tm, tn, u);
+            return hipGetLastError();
+        };
+        if (g.K % (BK * NSTAGE) != 0) return launch(update_kernel<R, TB, true, true, kLast>);
+        if (g.M % R != 0 || g.N % R != 0) return launch(update_kernel<R, TB, true, false, kLast>);
+        return launch(update_kernel<R, TB, false, false, kLast>);
+    };
+    auto tiles = [&](int R) { return (int64_t)((g.M + R - 1) / R) * ((g.N + R - 1) / R) * g.batch; };
+    auto size = [&](auto rc) { return last ? go(rc, std::true_type{}) : go(rc, std::false_type{}); };
+    return use128(tiles(256), tiles(128)) ? size(std::integral_constant<int, 128>{})
+                                          : size(std::integral_constant<int, 256>{});
+}
+
+template <bool TA, bool TB>
+hipError_t gram(const Plan& p, const GemmParams& g, _Float16* S, float f, uint8_t* ws,
+                hipStream_t s) {
+    if (p.splits == 1) return symmetric<TA, TB, false>(g, S, nullptr, p.lds, p.s_size, f, 0.0f, s);
+    float* partial = reinterpret_cast<float*>(ws + p.partial);
+    const unsigned tiles = (unsigned)lower_tiles(p.n, kGramTile);
+    const dim3 grid(tiles, p.splits, p.batch);
+    if (g.K % (BK * NSTAGE) != 0)
+        hipLaunchKernelGGL((gram_part_kernel<TA, TB, true>), grid, dim3(NT), 0, s, g, p.kc,
+                           p.splits, partial);
+    else
+        hipLaunchKernelGGL((gram_part_kernel<TA, TB, false>), grid, dim3(NT), 0, s, g, p.kc,
+                           p.splits, partial);
+    hipLaunchKernelGGL(gram_join_kernel, dim3(tiles, kGramTile / 16, p.batch), dim3(NT), 0, s,
+                       partial, p.splits, p.n, S, p.lds, p.s_size, f);
+    return hipGetLastError();
 }
 
 template <In T>
-void launch_init(const Plan& p, const Call& c, hipStream_t s) {
+hipError_t init(const Plan& p, const Call& c, _Float16* hi, _Float16* lo, hipStream_t s) {
     using E = typename InFmt<T>::S;
     const E* G = static_cast<const E*>(c.G);
     double* parts = reinterpret_cast<double*>(c.ws + p.parts);
+    const bool vec = rows_16b_aligned(G, c.ldg, sizeof(E)) && c.stride_g * sizeof(E) % 16 == 0;
     hipLaunchKernelGGL(norm_kernel<T>, dim3(kNormParts, p.batch), dim3(NT), 0, s, G, c.ldg,
-                       c.stride_g, p.M, p.N, parts);
-    hipLaunchKernelGGL(init_kernel<T>, dim3(grid_for(p.x_size), p.batch), dim3(NT), 0, s, G, c.ldg,
-                       c.stride_g, p.M, p.N, parts, (double)c.eps, std::ldexp(1.0, scale_exp(p)),
-                       reinterpret_cast<_Float16*>(c.ws + p.hi[0]),
-                       reinterpret_cast<_Float16*>(c.ws + p.lo[0]), p.ldx);
+                       c.stride_g, p.M, p.N, vec, parts);
+    hipLaunchKernelGGL(init_kernel<T>, dim3(grid_for(p.x_size / 8), p.batch), dim3(NT), 0, s, G,
+                       c.ldg, c.stride_g, p.M, p.N, vec, parts, (double)c.eps,
+                       std::ldexp(1.0, scale_exp(p)), hi, lo, p.ldx);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
-    if (c.t == In::F32) launch_init<In::F32>(p, c, s);
-    else if (c.t == In::BF16) launch_init<In::BF16>(p, c, s);
-    else launch_init<In::F16>(p, c, s);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    auto half = [&](int64_t at) { return reinterpret_cast<_Float16*>(c.ws + at); };
+    _Float16* hi[2] = {half(p.hi[0]), half(p.hi[1])};
+    _Float16* lo[2] = {half(p.lo[0]), half(p.lo[1])};
+    _Float16 *S = half(p.gram), *B = half(p.poly);
+    hipError_t e = c.t == In::F32    ? init<In::F32>(p, c, hi[0], lo[0], s)
+                   : c.t == In::BF16 ? init<In::BF16>(p, c, hi[0], lo[0], s)
+                                     : init<In::F16>(p, c, hi[0], lo[0], s);
     const bool tall = p.M > p.N;
-    const int n = p.s, large = tall ? p.M : p.N;
-    _Float16* hi[2] = {reinterpret_cast<_Float16*>(c.ws + p.hi[0]),
-                       reinterpret_cast<_Float16*>(c.ws + p.hi[1])};
-    _Float16* lo[2] = {reinterpret_cast<_Float16*>(c.ws + p.lo[0]),
-                       reinterpret_cast<_Float16*>(c.ws + p.lo[1])};
-    _Float16* S = reinterpret_cast<_Float16*>(c.ws + p.gram);
-    _Float16* B = reinterpret_cast<_Float16*>(c.ws + p.poly);
-    float* C = reinterpret_cast<float*>(c.ws + p.c32);
     const float xs = std::ldexp(1.0f, scale_exp(p));
-    const int64_t s_total = p.batch * p.s_size;
-    for (int i = 0; i < c.steps; ++i) {
+    Update u = {};
+    u.ldx = p.ldx; u.x_size = p.x_size;
+    u.a = c.a; u.f = 1.0f / kPolyScale;
+    u.O = c.O; u.ldo = c.ldo; u.stride_o = c.stride_o;
+    u.out_scale = 1.0f / xs;
+    u.o_vec = rows_16b_aligned(c.O, c.ldo, 2) && c.stride_o % 8 == 0;
+    for (int i = 0; i < c.steps && e == hipSuccess; ++i) {
         const int r = i & 1, w = 1 - r;
         // S: rows of X against rows (wide), columns against columns (tall)
-        e = product(p, n, n, large, hi[r], p.ldx, p.x_size, tall, hi[r], p.ldx, p.x_size, !tall, C,
-                    p.lds, p.s_size, s);
+        GemmParams g = operands(p, p.n, p.n, p.k, hi[r], p.ldx, p.x_size, hi[r], p.ldx, p.x_size);
+        const float fs = kGramScale / (xs * xs);
+        e = tall ? gram<true, false>(p, g, S, fs, c.ws, s) : gram<false, true>(p, g, S, fs, c.ws, s);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(gram_kernel, dim3(grid_for(s_total)), dim3(NT), 0, s, C, S, s_total,
-                           kGramScale / (xs * xs));
-        // S is symmetric: its rows serve as the columns
-        e = product(p, n, n, n, S, p.lds, p.s_size, 0, S, p.lds, p.s_size, 1, C, p.lds, p.s_size, s);
+        g = operands(p, p.n, p.n, p.n, S, p.lds, p.s_size, S, p.lds, p.s_size);
+        e = symmetric<false, true, true>(g, B, S, p.lds, p.s_size,
+                                         c.c * (kPolyScale / (kGramScale * kGramScale)),
+                                         c.b * (kPolyScale / kGramScale), s);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(poly_kernel, dim3(grid_for(s_total)), dim3(NT), 0, s, C, S, B, s_total,
-                           c.b * (kPolyScale / kGramScale),
-                           c.c * (kPolyScale / (kGramScale * kGramScale)));
-        if (tall)
-            e = product(p, p.M, p.N, n, hi[r], p.ldx, p.x_size, 0, B, p.lds, p.s_size, 1, C, p.ldx,
-                        p.x_size, s);
-        else
-            e = product(p, p.M, p.N, n, B, p.lds, p.s_size, 0, hi[r], p.ldx, p.x_size, 0, C, p.ldx,
-                        p.x_size, s);
-        if (e != hipSuccess) return e;
-        const dim3 grid(grid_for(p.x_size), p.batch);
-        if (i + 1 == c.steps)
-            hipLaunchKernelGGL(update_kernel<true>, grid, dim3(NT), 0, s, C, hi[r], lo[r], p.M, p.N,
-                               p.ldx, c.a, 1.0f / kPolyScale, nullptr, nullptr, c.O, c.ldo,
-                               c.stride_o, 1.0f / xs);
-        else
-            hipLaunchKernelGGL(update_kernel<false>, grid, dim3(NT), 0, s, C, hi[r], lo[r], p.M, p.N,
-                               p.ldx, c.a, 1.0f / kPolyScale, hi[w], lo[w], nullptr, 0, 0, 1.0f);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        u.hi = hi[r]; u.lo = lo[r];
+        u.hi2 = hi[w]; u.lo2 = lo[w];
+        const bool last = i + 1 == c.steps;
+        if (tall) {
+            g = operands(p, p.M, p.N, p.n, hi[r], p.ldx, p.x_size, B, p.lds, p.s_size);
+            g.tb = 1;
+            e = update<true>(g, u, last, s);
+        } else {
+            g = operands(p, p.M, p.N, p.n, B, p.lds, p.s_size, hi[r], p.ldx, p.x_size);
+            e = update<false>(g, u, last, s);
+        }
     }
-    return hipSuccess;
+    return e;
 }
 
 }  // namespace orth

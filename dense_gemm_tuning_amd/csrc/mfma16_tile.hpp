@@ -202,8 +202,9 @@ struct MnOperand {
 // R: workgroup tile R x R (256: one workgroup per CU; 128: two).
 // One R x R output tile at (m0, n0) over k = 0 .. p.K-1 of p's operands:
 // the body of mfma16_dma_kernel, shared with the stream-K kernel and the
-// Newton-Schulz products.  With an Epi of the caller's, epi(acc, wm, wn, lane)
-// gets the sums (wm, wn: the wavefront's place in the 2 x 2 grid).  Otherwise
+// Newton-Schulz products.  With an Epi of the caller's, epi(acc, wm, wn, lane,
+// mem) gets the sums (wm, wn: the wavefront's place in the 2 x 2 grid; mem: a
+// quarter of A's stages, the wavefront's own from here on).  Otherwise
 // raw == nullptr: the BLAS epilogue into p.C; or the bare fp32 sums go to
 // raw (R x R, row pitch R, every element written; a stream-K partial tile).
 struct BlasEpilogue {};
@@ -384,7 +385,10 @@ __device__ __forceinline__ void dma_tile(const GemmParams& p, int m0, int n0, fl
     DMA_WAIT_VMCNT(0);  // no copy may still target LDS when the workgroup ends
 
     if constexpr (!std::is_same<Epi, BlasEpilogue>::value) {
-        epi(acc, wm, wn, lane);
+        __syncthreads();  // no wavefront still reads the stages
+        uint8_t* mem = AK ? (wave < 2 ? sA0 : sA1) + (wave & 1) * (SA01 / 2)
+                          : wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sA2 : sA3;
+        epi(acc, wm, wn, lane, mem);
         return;
     }
     // 32x32 accumulator layout: register r of lane l is row
