@@ -498,23 +498,83 @@ def gemm_stream(A, B, C, alpha: float = 1.0, beta: float = 0.0, workspace=None, 
                         ws_bytes, _stream_handle(stream))
 
 
+# The calls below are made for decode steps of a few microseconds, so their
+# checks read every tensor attribute once and ask the library nothing.
+
+_FLOAT_CODES = None  # torch dtype -> enum gemm_dtype
+
+
 def _float_code(t, name):
-    import torch
-    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-    if t.dtype not in codes:
+    global _FLOAT_CODES
+    if _FLOAT_CODES is None:
+        import torch
+        _FLOAT_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
+                        torch.float16: DTYPE_F16}
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
-def _call_on(device, stream, call):
-    """call(stream handle) with ``device`` the current GPU and, by default,
-    the stream current there (a tensor may live on another GPU than the one
-    the caller has current)."""
+def _matrix(t, name):
+    """(rows, columns, row pitch) of a row-major 2-D tensor; for an empty or
+    single-row one, whose pitch is never used, a legal pitch."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {len(shape)}")
+    rows, cols = shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must be row-major with unit column stride")
+    if rows <= 1 or cols == 0:
+        pitch = max(pitch, cols, 1)
+    return rows, cols, pitch
+
+
+def _bytes(t, name, rows):
+    """(columns, pitch) of MX4 codes or scales of ``rows`` rows."""
     import torch
-    if hasattr(stream, "device") and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.device(device):
-        return call(_stream_handle(stream))
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be uint8, got {t.dtype}")
+    have, cols, pitch = _matrix(t, name)
+    if have != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {have}")
+    if rows <= 1 or cols == 0:
+        pitch = max(16, (cols + 15) // 16 * 16)
+    return cols, pitch
+
+
+def _fits(K, cols_q, cols_s, name):
+    need_q, need_s = (K + 31) // 32 * 16, (K + 511) // 512 * 16  # gemm_mx4_*_pitch
+    if cols_q < need_q or cols_s < need_s:
+        raise ValueError(f"{name}: {K} elements need rows of {need_q} code and {need_s} scale "
+                         f"bytes, got {cols_q} and {cols_s}")
+
+
+def _on_device(index, named):
+    """Every non-empty (name, tensor) on GPU ``index`` (-1: the host)."""
+    for name, t in named:
+        if (index < 0 or t.get_device() != index) and t.numel() > 0:
+            at = "a GPU" if index < 0 else f"cuda:{index}"
+            raise ValueError(f"{name} must be a GPU tensor on {at}, got {t.device}")
+
+
+def _call_on(index, stream, fn, *args):
+    """fn(*args, stream handle) with GPU ``index`` current and, by default, the
+    stream current there (the tensors may live on another GPU than the one the
+    caller has current)."""
+    import torch
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        at = getattr(stream, "device", None)
+        if at is not None and at.index != index:
+            raise ValueError(f"stream is on {at}, the tensors on cuda:{index}")
+        handle = getattr(stream, "cuda_stream", stream)
+    if torch.cuda.current_device() == index:
+        return fn(*args, handle)
+    with torch.cuda.device(index):
+        return fn(*args, handle)
 
 
 def mx4_empty(rows: int, K: int, device="cuda"):
@@ -525,59 +585,40 @@ def mx4_empty(rows: int, K: int, device="cuda"):
             torch.empty(rows, gemm_mx4_scale_pitch(K), dtype=torch.uint8, device=device))
 
 
-def _check_mx4(rows, K, Q, S, name):
-    """An MX4 operand of ``rows`` rows and K elements: uint8 codes
-    [rows, >= code pitch] and scales [rows, >= scale pitch]."""
-    import torch
-    if Q.dtype != torch.uint8 or S.dtype != torch.uint8:
-        raise TypeError(f"{name} codes and scales must be uint8")
-    _check_layout(((f"{name} codes", Q), (f"{name} scales", S)))
-    if Q.shape[0] != rows or S.shape[0] != rows:
-        raise ValueError(f"{name} codes and scales must have {rows} rows, got {Q.shape[0]} and "
-                         f"{S.shape[0]}")
-    if Q.shape[1] < gemm_mx4_code_pitch(K) or S.shape[1] < gemm_mx4_scale_pitch(K):
-        raise ValueError(f"{name}: {K} elements need rows of {gemm_mx4_code_pitch(K)} code and "
-                         f"{gemm_mx4_scale_pitch(K)} scale bytes, got {Q.shape[1]} and "
-                         f"{S.shape[1]}")
-
-
-def _pitch16(t) -> int:
-    """Row pitch of codes or scales; that of a single-row or empty operand is
-    never used, so report the next multiple of 16 bytes."""
-    return t.stride(0) if t.shape[0] > 1 and t.numel() > 0 else max(16, (t.shape[1] + 15) // 16 * 16)
-
-
 def quantize_mx4(X, Q, S, trans: bool = False, stream=None) -> int:
     """(Q, S) <- op(X) in MX4 blocks along its columns (gemm_mx4_quantize);
     op(X) is X, or X transposed when ``trans``.  X is float32, bfloat16 or
-    float16, row-major; Q and S as ``mx4_empty`` makes them for op(X).  Blocks run along
-    the summation index of the product the operand is for.  Returns the status
-    code."""
+    float16, row-major; Q and S as ``mx4_empty`` makes them for op(X).  Blocks
+    run along the summation index of the product the operand is for.  Returns
+    the status code."""
     dtype = _float_code(X, "X")
-    _check_layout((("X", X),))
-    M, K = X.shape[::-1] if trans else X.shape
-    _check_mx4(M, K, Q, S, "Q, S:")
-    _check_device((("X", X), ("Q", Q), ("S", S)), Q.device)
+    rows, cols, ldx = _matrix(X, "X")
+    M, K = (cols, rows) if trans else (rows, cols)
+    cols_q, ldq = _bytes(Q, "Q (codes)", M)
+    cols_s, lds = _bytes(S, "S (scales)", M)
+    _fits(K, cols_q, cols_s, "Q, S")
+    index = Q.get_device()
+    _on_device(index, (("X", X), ("Q", Q), ("S", S)))
     if M == 0 or K == 0:
         return GEMM_OK
-    return _call_on(Q.device, stream, lambda s: gemm_mx4_quantize(
-        dtype, trans, M, K, X.data_ptr(), _ld(X), Q.data_ptr(), _pitch16(Q), S.data_ptr(),
-        _pitch16(S), s))
+    return _call_on(index, stream, _load().gemm_mx4_quantize, dtype, int(trans), M, K,
+                    X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), lds)
 
 
 def dequantize_mx4(Q, S, Y, stream=None) -> int:
     """Y [rows, K] <- the values of an MX4 operand (gemm_mx4_dequantize), Y
     float32, bfloat16 or float16, row-major.  Returns the status code."""
     dtype = _float_code(Y, "Y")
-    _check_layout((("Y", Y),))
-    M, K = Y.shape
-    _check_mx4(M, K, Q, S, "Q, S:")
-    _check_device((("Q", Q), ("S", S), ("Y", Y)), Y.device)
+    M, K, ldy = _matrix(Y, "Y")
+    cols_q, ldq = _bytes(Q, "Q (codes)", M)
+    cols_s, lds = _bytes(S, "S (scales)", M)
+    _fits(K, cols_q, cols_s, "Q, S")
+    index = Y.get_device()
+    _on_device(index, (("Q", Q), ("S", S), ("Y", Y)))
     if M == 0 or K == 0:
         return GEMM_OK
-    return _call_on(Y.device, stream, lambda s: gemm_mx4_dequantize(
-        dtype, M, K, Q.data_ptr(), _pitch16(Q), S.data_ptr(), _pitch16(S), Y.data_ptr(), _ld(Y),
-        s))
+    return _call_on(index, stream, _load().gemm_mx4_dequantize, dtype, M, K, Q.data_ptr(), ldq,
+                    S.data_ptr(), lds, Y.data_ptr(), ldy)
 
 
 def gemm_quantized(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=None,
@@ -589,42 +630,49 @@ def gemm_quantized(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=
     summation runs over every stored element: codes past a ragged K are zeros
     (quantize_mx4 writes them so).  Returns the status code."""
     import torch
-    if C.dtype != torch.float32:
+    if C.dtype is not torch.float32:
         raise TypeError("C must be float32")
-    _check_layout((("A", A), ("C", C)))
-    M, N = C.shape
-    named = [("A", A), ("B", B), ("SB", SB), ("C", C)]
+    M, N, ldc = _matrix(C, "C")
+    rows_a, cols_a, lda = _matrix(A, "A")
+    cols_b, ldb = _bytes(B, "B (codes)", N)
+    cols_sb, ldsb = _bytes(SB, "SB (scales)", N)
+    index = C.get_device()
     if SA is None:
-        if A.dtype not in (torch.bfloat16, torch.float16):
+        if A.dtype is torch.float32 or A.dtype is torch.uint8:
             raise TypeError("A must be bfloat16 or float16, or MX4 codes with their scales SA")
-        K = A.shape[1]
-        if A.shape[0] != M:
+        dtype = _float_code(A, "A")
+        K = cols_a
+        if rows_a != M:
             raise ValueError(f"shape mismatch: A {tuple(A.shape)}, C {tuple(C.shape)}")
     else:
-        K = 2 * min(A.shape[1], B.shape[1])
-        if gemm_mx4_code_pitch(K) != 16 * (K // 32) or A.shape[1] != B.shape[1]:
+        _, lda = _bytes(A, "A (codes)", M)
+        cols_sa, ldsa = _bytes(SA, "SA (scales)", M)
+        K = 2 * cols_a
+        if cols_a != cols_b or cols_a % 16 != 0:
             raise ValueError("A and B must have code rows of one length, a multiple of 16 bytes, "
-                             f"got {A.shape[1]} and {B.shape[1]}")
-        _check_mx4(M, K, A, SA, "A, SA:")
-        named.append(("SA", SA))
-    _check_mx4(N, K, B, SB, "B, SB:")
+                             f"got {cols_a} and {cols_b}")
+        _fits(K, cols_a, cols_sa, "A, SA")
+    _fits(K, cols_b, cols_sb, "B, SB")
     bias_ptr = 0
     if bias is not None:
-        if bias.dtype != torch.float32 or bias.dim() != 1 or bias.shape[0] != N:
+        if bias.dtype is not torch.float32 or bias.dim() != 1 or bias.shape[0] != N:
             raise ValueError("bias must be float32 [N]")
-        _check_layout((("bias", bias),), dims=(1,))
-        named.append(("bias", bias))
+        if N > 1 and bias.stride(0) != 1:
+            raise ValueError("bias must be contiguous")
         bias_ptr = bias.data_ptr()
-    _check_device(named, C.device)
+        _on_device(index, (("bias", bias),))
+    _on_device(index, (("A", A), ("B", B), ("SB", SB), ("C", C)))
+    if SA is not None:
+        _on_device(index, (("SA", SA),))
     if M == 0 or N == 0:
         return GEMM_OK
-    tail = (B.data_ptr(), _pitch16(B), SB.data_ptr(), _pitch16(SB), float(beta), C.data_ptr(),
-            _ld(C), bias_ptr)
     if SA is None:
-        return _call_on(C.device, stream, lambda s: gemm_mx4_a16(
-            _float_code(A, "A"), M, N, K, float(alpha), A.data_ptr(), _ld(A), *tail, s))
-    return _call_on(C.device, stream, lambda s: gemm_mx4(
-        M, N, K, float(alpha), A.data_ptr(), _pitch16(A), SA.data_ptr(), _pitch16(SA), *tail, s))
+        return _call_on(index, stream, _load().gemm_mx4_a16, dtype, M, N, K, alpha, A.data_ptr(),
+                        lda, B.data_ptr(), ldb, SB.data_ptr(), ldsb, beta, C.data_ptr(), ldc,
+                        bias_ptr)
+    return _call_on(index, stream, _load().gemm_mx4, M, N, K, alpha, A.data_ptr(), lda,
+                    SA.data_ptr(), ldsa, B.data_ptr(), ldb, SB.data_ptr(), ldsb, beta,
+                    C.data_ptr(), ldc, bias_ptr)
 
 
 def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
@@ -634,12 +682,12 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     the default coefficients are the quintic's that Muon uses).  G is float32,
     bfloat16 or float16 and O bfloat16, both [M, N] or [batch, M, N] with
     row-major matrices; O may be G.  ``workspace`` is a contiguous GPU tensor
-    of at least gemm_orthogonalize_workspace_size bytes that no other call uses at
-    the same time; when None one is allocated here with torch, for the stream
-    the work runs on.  Returns the status code."""
+    of at least gemm_orthogonalize_workspace_size bytes that no other call uses
+    at the same time; when None one is allocated here with torch, for the
+    stream the work runs on.  Returns the status code."""
     import torch
     dtype = _float_code(G, "G")
-    if O.dtype != torch.bfloat16:
+    if O.dtype is not torch.bfloat16:
         raise TypeError("O must be bfloat16")
     _check_layout((("G", G), ("O", O)), dims=(2, 3))
     if G.shape != O.shape:
@@ -649,7 +697,8 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         named.append(("workspace", workspace))
-    _check_device(named, O.device)
+    index = O.get_device()
+    _on_device(index, named)
     if G.numel() == 0:
         return GEMM_OK
     M, N = G.shape[-2:]
@@ -663,12 +712,14 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     if need < 0:
         return need
     if workspace is None:
-        with torch.cuda.device(O.device):
-            handle = _stream_handle(stream)
-            on = torch.cuda.ExternalStream(handle, device=O.device) if stream is not None else None
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
+        else:  # in that stream's order, so that a later call cannot get it too early
+            on = (stream if hasattr(stream, "cuda_stream")
+                  else torch.cuda.ExternalStream(stream, device=O.device))
             with torch.cuda.stream(on):
                 workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
-    a, b, c = (float(v) for v in coefficients)
-    return _call_on(O.device, stream, lambda s: gemm_orthogonalize(
-        dtype, M, N, G2.data_ptr(), _ld(G2), sg, O2.data_ptr(), _ld(O2), so, batch, steps, a, b, c,
-        float(eps), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    a, b, c = coefficients
+    return _call_on(index, stream, _load().gemm_orthogonalize, dtype, M, N, G2.data_ptr(), _ld(G2),
+                    sg, O2.data_ptr(), _ld(O2), so, batch, steps, a, b, c, eps,
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
