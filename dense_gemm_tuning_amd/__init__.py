@@ -555,8 +555,8 @@ def _on_device(index, named):
     """Every non-empty (name, tensor) on GPU ``index`` (-1: the host)."""
     for name, t in named:
         if (index < 0 or t.get_device() != index) and t.numel() > 0:
-            at = "a GPU" if index < 0 else f"cuda:{index}"
-            raise ValueError(f"{name} must be a GPU tensor on {at}, got {t.device}")
+            at = "" if index < 0 else f" on cuda:{index}"
+            raise ValueError(f"{name} must be a GPU tensor{at}, got {t.device}")
 
 
 def _call_on(index, stream, fn, *args):
