@@ -105,7 +105,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
     const int rowsA = min(16 * RBT, p.M - mbase);
     const int nsteps = (nb + G::STEPB - 1) / G::STEPB;
     const int first = (int)((unsigned)q8 % (unsigned)nsteps);
-    auto at = [&](int s) INLINE { return s + first < nsteps ? s + first : s + first - nsteps; };
+    auto at = [&](int s) DGT_INLINE { return s + first < nsteps ? s + first : s + first - nsteps; };
 
     // One descriptor per operand, ending with the last valid row (rows past
     // it read as zeros).  A's 16-bit rows end on a whole 16-byte piece.
@@ -134,13 +134,13 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
     const uint32_t sprow = (uint32_t)(16 * ((nb + 15) / 16));
     // whether the wave's j-th of these is A's (known at compile time but for
     // a j that has some of each)
-    auto is_a = [&](auto jc) INLINE {
+    auto is_a = [&](auto jc) DGT_INLINE {
         constexpr int x0 = NWAVE * decltype(jc)::value;
         if constexpr (x0 + NWAVE <= G::NA) return true;
         else if constexpr (x0 >= G::NA) return false;
         else return x0 + wave < G::NA;
     };
-    static_for<G::IX>([&](auto jc) INLINE {
+    static_for<G::IX>([&](auto jc) DGT_INLINE {
         constexpr int j = decltype(jc)::value;
         const int x = NWAVE * j + wave;
         if (is_a(jc)) {
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
 #pragma unroll
         for (int c = 0; c < CBW; ++c) acc[rb][c] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-    auto copy_step = [&](auto qc, int t) INLINE {
+    auto copy_step = [&](auto qc, int t) DGT_INLINE {
         uint8_t* st = dma::pick<decltype(qc)::value>(st0, st1, st2, st3);
         const int s = at(min(t, nsteps - 1));
         const int lim_b = t < nsteps ? nb - G::STEPB * s : 0;  // pieces left in a row
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
         for (int j = 0; j < G::IB; ++j)
             copy_piece<16, 2>(base_b, range_b, st + 1024 * (G::IB * wave + j),
                               cb[j] < lim_b ? voff_b[j] + (uint32_t)(ROWB * s) : 0xfffffff0u);
-        static_for<G::IX>([&](auto jc) INLINE {
+        static_for<G::IX>([&](auto jc) DGT_INLINE {
             constexpr int j = decltype(jc)::value;
             const int x = NWAVE * j + wave;
             if (is_a(jc))
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
     };
 
     // The wave's part of step s, in stage st; kCut: the row ends inside the step.
-    auto compute = [&](const uint8_t* st, auto cutc, int s) INLINE {
+    auto compute = [&](const uint8_t* st, auto cutc, int s) DGT_INLINE {
         constexpr bool kCut = decltype(cutc)::value;
         const uint8_t* sa_ = st + G::B_BYTES;
         const uint8_t* scales = sa_ + G::A_BYTES;
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
     // Step s in stage Q.  At the wait the wave's copies of steps s+1 .. s+NS-2
     // are newer than this step's.
     constexpr int kMost = G::IB + G::IX;
-    auto step = [&](auto qc, int s) INLINE {
+    auto step = [&](auto qc, int s) DGT_INLINE {
         constexpr int Q = decltype(qc)::value;
         const int k = at(s);
         if (wave < G::XREST) {
@@ -288,10 +288,10 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
         if (kBlock * G::STEPB * (k + 1) > p.K) compute(st, std::true_type{}, k);
         else compute(st, std::false_type{}, k);
     };
-    static_for<NS - 1>([&](auto qc) INLINE { copy_step(qc, decltype(qc)::value); });
+    static_for<NS - 1>([&](auto qc) DGT_INLINE { copy_step(qc, decltype(qc)::value); });
     fence();
     for (int s = 0; s < nsteps; s += NS) {  // stages are compile-time
-        static_for<NS>([&](auto jc) INLINE {
+        static_for<NS>([&](auto jc) DGT_INLINE {
             constexpr int j = decltype(jc)::value;
             if (s + j < nsteps) step(jc, s + j);
         });
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
     constexpr int RR = kFit >= 16 ? 16 : kFit >= 8 ? 8 : 4;
     static_assert(RR * KS * COLS * 4 <= G::STAGE, "a pass fits a stage");
     dma::barrier();
-    static_for<RBT * 16 / RR>([&](auto pc) INLINE {
+    static_for<RBT * 16 / RR>([&](auto pc) DGT_INLINE {
         constexpr int pass = decltype(pc)::value, rb = pass * RR / 16, r0 = pass * RR % 16;
         float* red = reinterpret_cast<float*>(dma::pick<pass % 2>(st0, st1, st0, st0));
         if (4 * g >= r0 && 4 * g < r0 + RR) {

@@ -149,7 +149,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
 
     // Copy group cp of step s into ring stage Q (chunks past the row's end,
     // and steps past the wave's range, read as zeros without memory traffic).
-    auto issue = [&](auto qc, auto cpc, int s) INLINE {
+    auto issue = [&](auto qc, auto cpc, int s) DGT_INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         uint8_t* dst = dma::pick<Q>(st0, st1, st2, st3) + STAGE * wave;
         const int lim = s < s1 ? nb - G::STEPB * s : 0;
@@ -159,14 +159,14 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
             copy_b(gbase[cp], grange[cp], dst + 1024 * j, voff);
         }
     };
-    auto load_scale = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t off) INLINE -> uint32_t {
+    auto load_scale = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t off) DGT_INLINE -> uint32_t {
         if constexpr (U == 4) return __builtin_amdgcn_raw_buffer_load_b32(rs, (int)off, 0, 0);
         else return (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)off, 0, 0);
     };
     // A and the scales of step s (past the last step: the last one's).
     // Always LA vector loads, which the waits below count on; a cut-off step
     // of 16-bit A may issue fewer and waits for everything instead.
-    auto load_ops = [&](int s, Ops& o) INLINE {
+    auto load_ops = [&](int s, Ops& o) DGT_INLINE {
         s = min(s, nsteps - 1);
         const int b0 = G::STEPB * s + U * g;  // the lane's first block
 #pragma unroll
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         } else {
             const bool cut = kBlock * G::STEPB * (s + 1) > p.K;  // uniform
             // piece e of the lane: 8 k from here
-            auto at = [&](int e) INLINE {
+            auto at = [&](int e) DGT_INLINE {
                 return KA == Kind::F16 ? kBlock * (G::STEPB * s + e) + 8 * g : kBlock * b0 + 8 * e;
             };
             if (!cut) {
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         }
     };
     // Scale bytes past the last block (in the row's last step) become 2^0.
-    auto mask_scales = [&](int s, Ops& o) INLINE {
+    auto mask_scales = [&](int s, Ops& o) DGT_INLINE {
         if (G::STEPB * (s + 1) <= nb) return;
         const int left = nb - (G::STEPB * s + U * g);
         const uint32_t keep = left <= 0 ? 0u : left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
             for (int rb = 0; rb < RB; ++rb) o.sa[rb] = (o.sa[rb] & keep) | (0x7f7f7f7fu & ~keep);
         }
     };
-    auto compute = [&](auto qc, auto cpc, const Ops& o) INLINE {
+    auto compute = [&](auto qc, auto cpc, const Ops& o) DGT_INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         const uint8_t* st = dma::pick<Q>(st0, st1, st2, st3) + STAGE * wave;
         if constexpr (KA == Kind::F16) {
@@ -279,9 +279,9 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
                 bop[b][u] = *reinterpret_cast<const u32x4*>(
                     st + (16 * b + i) * ROWB + (((U * g + u) ^ G::swz(16 * b + i)) << 4));
         __builtin_amdgcn_sched_barrier(0);  // keep them ahead of the products
-        static_for<G::NBK>([&](auto bc) INLINE {
+        static_for<G::NBK>([&](auto bc) DGT_INLINE {
             constexpr int b = decltype(bc)::value, c = G::NBK * cp + b;
-            static_for<U>([&](auto uc) INLINE {
+            static_for<U>([&](auto uc) DGT_INLINE {
                 constexpr int u = decltype(uc)::value;
                 if constexpr (KA == Kind::MX4) {
 #pragma unroll
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
     // too; not counting them only waits for more.  A load that waited for
     // everything (a cut-off step) leaves no older copy in flight, so the
     // counts hold after it as well.
-    auto phase = [&](auto qc, auto cpc, int s, Ops& o, Ops& next) INLINE {
+    auto phase = [&](auto qc, auto cpc, int s, Ops& o, Ops& next) DGT_INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         constexpr int ahead = cp + D;
         DMA_WAIT_VMCNT_LGKM0(63);  // this wave's reads of the stage have returned
@@ -335,17 +335,17 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         fence();
     };
     // Steps whose groups start at ring stage Q0.
-    auto step = [&](auto q0c, int s, Ops& o, Ops& next) INLINE {
+    auto step = [&](auto q0c, int s, Ops& o, Ops& next) DGT_INLINE {
         constexpr int Q0 = decltype(q0c)::value;
-        static_for<NG>([&](auto cpc) INLINE {
+        static_for<NG>([&](auto cpc) DGT_INLINE {
             phase(std::integral_constant<int, (Q0 + decltype(cpc)::value) % NS>{}, cpc, s, o, next);
         });
     };
 
     if (s0 < s1) {
         Ops o0, o1;
-        auto copies = [&]() INLINE {
-            static_for<D>([&](auto dc) INLINE {
+        auto copies = [&]() DGT_INLINE {
+            static_for<D>([&](auto dc) DGT_INLINE {
                 constexpr int d = decltype(dc)::value;
                 issue(dc, std::integral_constant<int, d % NG>{}, s0 + d / NG);
             });
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
         constexpr int kRing = NS > NG ? NS / NG : 1;
         constexpr int kUnroll = kRing > 2 ? kRing : 2;
         for (int s = s0; s < s1; s += kUnroll) {
-            static_for<kUnroll>([&](auto jc) INLINE {
+            static_for<kUnroll>([&](auto jc) DGT_INLINE {
                 constexpr int j = decltype(jc)::value;
                 if (s + j >= s1) return;
                 using Q0 = std::integral_constant<int, (j * NG) % NS>;

@@ -107,22 +107,42 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-    auto frags = [&](auto Jc, int s, u32x4 (&a)[TM], u32x4 (&b)[TM]) {
+    auto frags = [&](auto Jc, int s, u32x4 (&a)[TM], u32x4 (&b)[TM]) DGT_INLINE {
         constexpr int J = decltype(Jc)::value;
         opa.frags(pick<J / 2>(sA0, sA1, sA0, sA0), J % 2, s, a);
         opb.frags(pick<J / 2>(sB0, sB1, sB0, sB0), J % 2, s, b);
     };
-    auto copy_scales = [&](int g) {
+    // Half `half` of pair pr of an operand's slices.  When the last group is
+    // cut by the row's end (kTail), the chunks at or past nb read as zeros,
+    // so a row is whole groups for the loop.
+    int chunk[Geo<R>::KC_INSTR];  // of the lane, in a pair's row
+#pragma unroll
+    for (int i = 0; i < Geo<R>::KC_INSTR; ++i)
+        chunk[i] = (lane & 7) ^ swz_kc(8 * (Geo<R>::KC_INSTR * wave + i) + (lane >> 3));
+    auto copy = [&](const Op& op, uint8_t* st, int pr, int half) DGT_INLINE {
+        if constexpr (!kTail) {
+            op.template copy<kEdge, false>(st, pr, half, wave);
+        } else {
+            constexpr int HALF = Geo<R>::KC_INSTR / 2;
+            const int left = nb - 8 * pr;
+#pragma unroll
+            for (int i = HALF * half; i < HALF * half + HALF; ++i)
+                dma16(op.base, op.bytes, st + (Geo<R>::KC_INSTR * wave + i) * 1024,
+                      chunk[i] < left ? op.voff[i] : 0xfffffff0u, (uint32_t)pr * 128u);
+        }
+    };
+    auto copy_scales = [&](int g) DGT_INLINE {
         g = g < groups ? g : groups - 1;  // past the end: the last group, never used
 #pragma unroll
         for (int i = 0; i < SC; ++i) sc[i].copy(sS, g);
     };
     // The scales of group g for this lane's rows.  Blocks at or past nb (in
-    // the last group) get the neutral scale 1; their codes are masked.
+    // the last group) get the scale 1: what is stored there may be the NaN scale, and
+    // their codes are zero.
     u32x4 sa[TM], sb[TM];
     const int srow_a = 16 * (wm * (R / 2) + (lane & 31));
     const int srow_b = 16 * (R + wn * (R / 2) + (lane & 31));
-    auto read_scales = [&](int g) {
+    auto read_scales = [&](int g) DGT_INLINE {
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
             sa[t] = *reinterpret_cast<const u32x4*>(sS + srow_a + 512 * t);
@@ -135,17 +155,15 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
                 sa[t][d] >>= 8 * h;
                 sb[t][d] >>= 8 * h;
             }
-        if constexpr (kTail) {
-            if (16 * (g + 1) > nb) {
+        if constexpr (kTail) {  // every group: a branch here costs the loop its registers
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const int left = nb - (16 * g + 4 * d + h);  // blocks from byte 0 on
-                    const uint32_t keep = left <= 0 ? 0u : left <= 2 ? 0xffffu : 0xffffffffu;
+            for (int d = 0; d < 4; ++d) {
+                const int left = nb - (16 * g + 4 * d + h);  // blocks from byte 0 on
+                const uint32_t keep = left <= 0 ? 0u : left <= 2 ? 0xffffu : 0xffffffffu;
 #pragma unroll
-                    for (int t = 0; t < TM; ++t) {
-                        sa[t][d] = (sa[t][d] & keep) | (0x7f7f7f7fu & ~keep);
-                        sb[t][d] = (sb[t][d] & keep) | (0x7f7f7f7fu & ~keep);
-                    }
+                for (int t = 0; t < TM; ++t) {
+                    sa[t][d] = (sa[t][d] & keep) | (0x7f7f7f7fu & ~keep);
+                    sb[t][d] = (sb[t][d] & keep) | (0x7f7f7f7fu & ~keep);
                 }
             }
         }
@@ -154,7 +172,7 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
     // The products of step kS of slice kJ on (a, b); LDS reads and copies
     // are spread between them as in the 16-bit kernel, kReads of 16 bytes per
     // four products.
-    auto mfma_step = [&](auto Jc, auto Sc, auto Rc, const u32x4 (&a)[TM], const u32x4 (&b)[TM]) {
+    auto mfma_step = [&](auto Jc, auto Sc, auto Rc, const u32x4 (&a)[TM], const u32x4 (&b)[TM]) DGT_INLINE {
         constexpr int J = decltype(Jc)::value, kS = decltype(Sc)::value, kReads = decltype(Rc)::value;
 #pragma unroll
         for (int ti = 0; ti < TM; ++ti)
@@ -185,36 +203,20 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
     };
 
     u32x4 a0[TM], b0[TM], a1[TM], b1[TM];
-    // In a slice cut by the row's end the chunks at or past nb hold whatever
-    // follows in the row; they are cleared (step s: chunk 4kt + 2s + h).
-    auto mask_k = [&](int kt, int s, u32x4 (&f)[TM]) {
-        const uint32_t keep = 4 * kt + 2 * s + h < nb ? 0xffffffffu : 0u;
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[t][e] &= keep;
-    };
     // Slice kt at position J of its group: the copies, waits and barrier of the
     // 16-bit kernel with both operands k-contiguous (even slices copy the second half of
     // the next pair before the barrier, odd ones the first half of the pair
     // after it behind the barrier), plus the next group's scales after the
     // barrier of slice 0: newer than what slice 1's barrier publishes, so its
     // wait lets them through; slice 2's wait covers them.
-    auto slice = [&](auto Jc, int kt, auto maskc) {
+    auto slice = [&](auto Jc, int kt) DGT_INLINE {
         constexpr int J = decltype(Jc)::value;
         constexpr bool kEven = J % 2 == 0;
-        constexpr bool kMask = decltype(maskc)::value;
         using Two = std::integral_constant<int, 2>;
         frags(Jc, 1, a1, b1);
-        if constexpr (kMask) {
-            if (kt == nk - 1 && nb % 4 != 0) {
-                mask_k(kt, 0, a0); mask_k(kt, 1, a1);
-                mask_k(kt, 0, b0); mask_k(kt, 1, b1);
-            }
-        }
         if constexpr (kEven) {
-            opa.template copy<kEdge, kTail>(pick<(J / 2 + 1) % 2>(sA0, sA1, sA0, sA0), kt / 2 + 1, 1, wave);
-            opb.template copy<kEdge, kTail>(pick<(J / 2 + 1) % 2>(sB0, sB1, sB0, sB0), kt / 2 + 1, 1, wave);
+            copy(opa, pick<(J / 2 + 1) % 2>(sA0, sA1, sA0, sA0), kt / 2 + 1, 1);
+            copy(opb, pick<(J / 2 + 1) % 2>(sB0, sB1, sB0, sB0), kt / 2 + 1, 1);
         }
         mfma_step(Jc, std::integral_constant<int, 0>{}, Two{}, a0, b0);
         DMA_WAIT_VMCNT_LGKM0((copies_after<true, true, kEven>(CKC, 0) + (J == 1 ? SC : 0)));
@@ -222,38 +224,29 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
         frags(std::integral_constant<int, (J + 1) % 4>{}, 0, a0, b0);
         if constexpr (J == 0) copy_scales(kt / 4 + 1);
         if constexpr (!kEven) {
-            opa.template copy<kEdge, kTail>(pick<((J + 3) / 2) % 2>(sA0, sA1, sA0, sA0), (kt + 3) / 2, 0, wave);
-            opb.template copy<kEdge, kTail>(pick<((J + 3) / 2) % 2>(sB0, sB1, sB0, sB0), (kt + 3) / 2, 0, wave);
+            copy(opa, pick<((J + 3) / 2) % 2>(sA0, sA1, sA0, sA0), (kt + 3) / 2, 0);
+            copy(opb, pick<((J + 3) / 2) % 2>(sB0, sB1, sB0, sB0), (kt + 3) / 2, 0);
         }
         mfma_step(Jc, std::integral_constant<int, 1>{}, Two{}, a1, b1);
         if constexpr (J == 3) read_scales(kt / 4 + 1);
     };
 
     copy_scales(0);
-    opa.template copy<kEdge, kTail>(sA0, 0, 0, wave);
-    opa.template copy<kEdge, kTail>(sA0, 0, 1, wave);
-    opb.template copy<kEdge, kTail>(sB0, 0, 0, wave);
-    opb.template copy<kEdge, kTail>(sB0, 0, 1, wave);
-    opa.template copy<kEdge, kTail>(sA1, 1, 0, wave);
-    opb.template copy<kEdge, kTail>(sB1, 1, 0, wave);
+    copy(opa, sA0, 0, 0);
+    copy(opa, sA0, 0, 1);
+    copy(opb, sB0, 0, 0);
+    copy(opb, sB0, 0, 1);
+    copy(opa, sA1, 1, 0);
+    copy(opb, sB1, 1, 0);
     DMA_WAIT_VMCNT((prologue_after<true, true>(CKC, 0)));  // slice 0 and its scales landed
     barrier();
     frags(std::integral_constant<int, 0>{}, 0, a0, b0);
     read_scales(0);
-    using NoMask = std::false_type;
-    int kt = 0;
-    for (; kt + NSTAGE < nk + (kTail ? 0 : 1); kt += NSTAGE) {
-        slice(std::integral_constant<int, 0>{}, kt, NoMask{});
-        slice(std::integral_constant<int, 1>{}, kt + 1, NoMask{});
-        slice(std::integral_constant<int, 2>{}, kt + 2, NoMask{});
-        slice(std::integral_constant<int, 3>{}, kt + 3, NoMask{});
-    }
-    if constexpr (kTail) {  // the last group: 1 to 4 slices, the last possibly cut
-        const int rest = nk - kt;
-        slice(std::integral_constant<int, 0>{}, kt, std::true_type{});
-        if (rest >= 2) slice(std::integral_constant<int, 1>{}, kt + 1, std::true_type{});
-        if (rest >= 3) slice(std::integral_constant<int, 2>{}, kt + 2, std::true_type{});
-        if (rest >= 4) slice(std::integral_constant<int, 3>{}, kt + 3, std::true_type{});
+    for (int kt = 0; kt < NSTAGE * groups; kt += NSTAGE) {
+        slice(std::integral_constant<int, 0>{}, kt);
+        slice(std::integral_constant<int, 1>{}, kt + 1);
+        slice(std::integral_constant<int, 2>{}, kt + 2);
+        slice(std::integral_constant<int, 3>{}, kt + 3);
     }
     DMA_WAIT_VMCNT(0);  // no copy may still target LDS when the workgroup ends
 
@@ -274,16 +267,20 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
     auto at = [&](int ti, int tj, int r) -> float* {
         return &cbase[(int64_t)(ti * 32 + 8 * (r >> 2) + (r & 3)) * p.ldc + tj * 32];
     };
+    if (beta == 0.0f) {
 #pragma unroll
-    for (int ti = 0; ti < TM; ++ti)
+        for (int ti = 0; ti < TM; ++ti)
 #pragma unroll
-        for (int tj = 0; tj < TM; ++tj) {
-            if (beta == 0.0f) {
+            for (int tj = 0; tj < TM; ++tj)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     if (ok(ti, tj, r))
                         __builtin_nontemporal_store(alpha * acc[ti][tj][r] + bias[tj], at(ti, tj, r));
-            } else {
+    } else {
+#pragma unroll
+        for (int ti = 0; ti < TM; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TM; ++tj) {
                 float cv[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) cv[r] = ok(ti, tj, r) ? *at(ti, tj, r) : 0.0f;
@@ -293,7 +290,7 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
                         __builtin_nontemporal_store(
                             (alpha * acc[ti][tj][r] + beta * cv[r]) + bias[tj], at(ti, tj, r));
             }
-        }
+    }
 }
 
 template <int R>

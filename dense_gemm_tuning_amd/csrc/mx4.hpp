@@ -11,6 +11,10 @@
 
 #include "gemm_common.hpp"
 
+// For the kernels whose bodies are lambdas over register arrays: one that is
+// not inlined puts those arrays into scratch memory.
+#define DGT_INLINE __attribute__((always_inline))
+
 namespace dgt {
 namespace mx4 {
 

@@ -17,10 +17,6 @@ __device__ __forceinline__ intx8 widen(u32x4 x) {
     return intx8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
 }
 
-// The kernel's body is lambdas over register arrays: one that is not inlined
-// puts them into scratch memory.
-#define INLINE __attribute__((always_inline))
-
 // f(0), .., f(n-1) with compile-time arguments.
 template <int... I, typename F>
 __device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F&& f) {
