@@ -23,7 +23,7 @@ SOURCES = ["gemm_api.cpp", "k_naive.hip", "k_lds.hip", "k_mfma_f32.hip", "k_mfma
            "k_skinny_f32.hip",
            "k_splitk.hip", "mx4_api.cpp", "k_mx4_quant.hip", "k_mx4_tile.hip", "k_mx4_skinny.hip",
            "k_mx4_rows.hip", "orth_api.cpp",
-           "k_orth.hip"]
+           "k_orth.hip", "k_orth_small.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

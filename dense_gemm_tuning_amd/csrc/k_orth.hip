@@ -15,18 +15,17 @@
 // rounding X adds in the weak singular directions by up to a (3.4 with the
 // usual coefficients, 484 over five steps), so rounding X itself to 16 bits
 // costs a result normwise 2 to 4e-3 against 1.7e-3 that its own bf16 rounding costs.
-// X is therefore kept as two halves hi + lo (22 bits); the products read hi,
-// the term a X both.  What hi's rounding E adds through the products reaches the
-// weak directions only as (b S + c S S) E, small where S is, and the result
-// is 1.7 to 2.4e-3 off (matrices of 256 to 1024, normal, low-rank and 1/i spectra).
+// X is therefore kept as two halves hi + lo (22 bits) while more than two
+// steps are left; the products read hi, the term a X both.  What hi's rounding
+// E adds through the products reaches the weak directions only as (b S + c S S) E, small
+// where S is, and the result is 1.7 to 2.4e-3 off (matrices of 256 to
+// 1536, normal, low-rank, 1/i and 1/i^2 spectra; one half throughout: 2.2e-3 to 2e-2).
 //
 // FP16's range: |X| <= |X|_2, about 1, but its elements are near
 // 1/sqrt(max(M, N)) and the Gram matrix's smaller still, so X is held times
 // 2^x_exp near that root, S times 2^12 and the polynomial times 2^10 (both at most
 // about 13 * 2^10 for singular values up to 1.3); powers of two, so only the
 // range moves.
-#include <cmath>
-
 #include "mfma16_tile.hpp"
 #include "orth.hpp"
 
@@ -36,15 +35,6 @@ namespace orth {
 namespace {
 
 using namespace mfma16;
-
-constexpr float kGramScale = 4096.0f;  // 2^12
-constexpr float kPolyScale = 1024.0f;  // 2^10
-
-typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
-
-int scale_exp(const Plan& p) {  // round(log2(sqrt(max(M, N))))
-    return (int)std::lround(0.5 * std::log2((double)p.k));
-}
 
 // Eight elements of a row, widened; `vec`: the row starts and pitch are on 16
 // bytes.
@@ -184,25 +174,17 @@ struct Chunk {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = mem[at(r + e, c)];
     }
-    // fn(row, column, 8 values along the row) over the chunk, or with
-    // kMirror fn(column, row, 8 values down the column).
-    template <bool kMirror, typename Fn>
-    __device__ void each(int lane, Fn&& fn) const {
-#pragma unroll
-        for (int i = 0; i < 32 * W / 8 / 64; ++i) {
-            const int e = 64 * i + lane;
-            float v[8];
-            if constexpr (kMirror) {
-                const int c = e % W, r = e / W * 8;
-                col8(r, c, v);
-                fn(c, r, v);
-            } else {
-                const int r = e / GROUPS, c = e % GROUPS * 8;
-                row8(r, c, v);
-                fn(r, c, v);
-            }
-        }
+    void __device__ set_row8(int r, int c, const float (&v)[8]) const {
+        *reinterpret_cast<floatx4*>(mem + at(r, c)) = floatx4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<floatx4*>(mem + at(r, c + 4)) = floatx4{v[4], v[5], v[6], v[7]};
     }
+    // The lane's pieces of a chunk: piece i is 8 columns of a row, or
+    // (mirrored) 8 rows of a column.
+    static constexpr int PIECES = 32 * W / 8 / 64;
+    __device__ static int row(int i, int lane) { return (64 * i + lane) / GROUPS; }
+    __device__ static int col(int i, int lane) { return (64 * i + lane) % GROUPS * 8; }
+    __device__ static int mirror_col(int i, int lane) { return (64 * i + lane) % W; }
+    __device__ static int mirror_row(int i, int lane) { return (64 * i + lane) / W * 8; }
 };
 
 // Tiles on and below the diagonal, numbered row by row; XCD x takes a
@@ -232,47 +214,63 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void symmetric_kernel(
     const int m0 = tile.bm * R, n0 = tile.bn * R;
     dma_tile<In::F16, R, TA, TB, kEdge, kTail>(
         p, m0, n0, nullptr, [&](const auto& acc, int wm, int wn, int lane, uint8_t* mem) {
-            const Chunk<R> chunk{reinterpret_cast<float*>(mem)};
-            static_assert(32 * Chunk<R>::W * 4 <= (TA ? Geo<R>::MN_STAGE : Geo<R>::KC_STAGE / 2), "");
+            using Ch = Chunk<R>;
+            const Ch chunk{reinterpret_cast<float*>(mem)};
+            static_assert(32 * Ch::W * 4 <= (TA ? Geo<R>::MN_STAGE : Geo<R>::KC_STAGE / 2), "");
+            const int row0 = m0 + wm * (R / 2), col0 = n0 + wn * (R / 2);
+            // D one chunk ahead of its use
+            halfx8 d[2][kAdd ? Ch::PIECES : 1];
+            auto fetch = [&](int ti) {
+                if constexpr (kAdd) {
+#pragma unroll
+                    for (int i = 0; i < Ch::PIECES; ++i) {
+                        const int row = row0 + 32 * ti + Ch::row(i, lane), col = col0 + Ch::col(i, lane);
+                        if (!kEdge || (row < p.M && col < p.N))
+                            d[ti & 1][i] = *reinterpret_cast<const halfx8*>(add + row * ld + col);
+                    }
+                }
+            };
+            fetch(0);
 #pragma unroll
             for (int ti = 0; ti < Geo<R>::TM; ++ti) {
-                const int row0 = m0 + wm * (R / 2) + ti * 32, col0 = n0 + wn * (R / 2);
+                if (ti + 1 < Geo<R>::TM) fetch(ti + 1);
                 chunk.put(acc[ti], lane);
-                chunk.template each<false>(lane, [&](int r, int c, const float (&v)[8]) {
-                    const int row = row0 + r, col = col0 + c;
-                    if (kEdge && (row >= p.M || col >= p.N)) return;
+#pragma unroll
+                for (int i = 0; i < Ch::PIECES; ++i) {
+                    const int r = Ch::row(i, lane), c = Ch::col(i, lane);
+                    const int row = row0 + 32 * ti + r, col = col0 + c;
+                    float v[8];
+                    chunk.row8(r, c, v);
                     halfx8 o;
-                    if constexpr (kAdd) {
-                        const halfx8 d = *reinterpret_cast<const halfx8*>(add + row * ld + col);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = (_Float16)(f2 * (float)d[e] + f1 * v[e]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = (_Float16)(f1 * v[e]);
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = kAdd ? f2 * (float)d[ti & 1][i][e] + f1 * v[e] : f1 * v[e];
+                        o[e] = (_Float16)v[e];
                     }
-                    *reinterpret_cast<halfx8*>(out + row * ld + col) = o;
-                });
-                if (m0 != n0)  // D is symmetric too: its mirrored rows are read
-                    chunk.template each<true>(lane, [&](int c, int r, const float (&v)[8]) {
-                        const int row = col0 + c, col = row0 + r;
-                        if (kEdge && (row >= p.N || col >= p.M)) return;
-                        halfx8 o;
-                        if constexpr (kAdd) {
-                            const halfx8 d = *reinterpret_cast<const halfx8*>(add + row * ld + col);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                o[e] = (_Float16)(f2 * (float)d[e] + f1 * v[e]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = (_Float16)(f1 * v[e]);
-                        }
+                    if (kAdd && m0 != n0) chunk.set_row8(r, c, v);  // for the mirrored pieces
+                    if (!kEdge || (row < p.M && col < p.N))
                         *reinterpret_cast<halfx8*>(out + row * ld + col) = o;
-                    });
+                }
+                if (m0 == n0) continue;
+                if constexpr (kAdd) Ch::fence();
+#pragma unroll
+                for (int i = 0; i < Ch::PIECES; ++i) {
+                    const int c = Ch::mirror_col(i, lane), r = Ch::mirror_row(i, lane);
+                    const int row = col0 + c, col = row0 + 32 * ti + r;
+                    float v[8];
+                    chunk.col8(r, c, v);
+                    halfx8 o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = (_Float16)(kAdd ? v[e] : f1 * v[e]);
+                    if (!kEdge || (row < p.N && col < p.M))
+                        *reinterpret_cast<halfx8*>(out + row * ld + col) = o;
+                }
             }
         });
 }
 
-// X' = a (hi + lo) + f * sums: two halves, or (kLast) the result in bf16.
+// X' = a (hi + lo) + f * sums: two halves, or (kLast) the result in bf16.  lo
+// or lo2 is null where X or X' is kept in one half.
 struct Update {
     const _Float16 *hi, *lo;
     _Float16 *hi2, *lo2;
@@ -293,21 +291,39 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams
     uint16_t* O = u.O + tile.z * u.stride_o;
     dma_tile<In::F16, R, false, TB, kEdge, kTail>(
         p, m0, n0, nullptr, [&](const auto& acc, int wm, int wn, int lane, uint8_t* mem) {
-            const Chunk<R> chunk{reinterpret_cast<float*>(mem)};
+            using Ch = Chunk<R>;
+            const Ch chunk{reinterpret_cast<float*>(mem)};
+            const int row0 = m0 + wm * (R / 2), col0 = n0 + wn * (R / 2);
+            // X one chunk ahead of its use
+            halfx8 h[2][Ch::PIECES], l[2][Ch::PIECES];
+            auto fetch = [&](int ti) {
+#pragma unroll
+                for (int i = 0; i < Ch::PIECES; ++i) {
+                    const int row = row0 + 32 * ti + Ch::row(i, lane), col = col0 + Ch::col(i, lane);
+                    const int64_t at = xz + (int64_t)row * u.ldx + col;
+                    if (!kEdge || (row < p.M && col < p.N)) {
+                        h[ti & 1][i] = *reinterpret_cast<const halfx8*>(u.hi + at);
+                        if (u.lo) l[ti & 1][i] = *reinterpret_cast<const halfx8*>(u.lo + at);
+                        else l[ti & 1][i] = halfx8{};
+                    }
+                }
+            };
+            fetch(0);
 #pragma unroll
             for (int ti = 0; ti < Geo<R>::TM; ++ti) {
-                const int row0 = m0 + wm * (R / 2) + ti * 32, col0 = n0 + wn * (R / 2);
+                if (ti + 1 < Geo<R>::TM) fetch(ti + 1);
                 chunk.put(acc[ti], lane);
-                chunk.template each<false>(lane, [&](int r, int c, const float (&v)[8]) {
-                    const int row = row0 + r, col = col0 + c;
-                    if (kEdge && (row >= p.M || col >= p.N)) return;
-                    const int64_t at = xz + (int64_t)row * u.ldx + col;
-                    const halfx8 h = *reinterpret_cast<const halfx8*>(u.hi + at);
-                    const halfx8 l = *reinterpret_cast<const halfx8*>(u.lo + at);
+#pragma unroll
+                for (int i = 0; i < Ch::PIECES; ++i) {
+                    const int r = Ch::row(i, lane), c = Ch::col(i, lane);
+                    const int row = row0 + 32 * ti + r, col = col0 + c;
                     float x[8];
+                    chunk.row8(r, c, x);
+                    if (kEdge && (row >= p.M || col >= p.N)) continue;
+                    const int64_t at = xz + (int64_t)row * u.ldx + col;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        x[e] = u.a * ((float)h[e] + (float)l[e]) + u.f * v[e];
+                        x[e] = u.a * ((float)h[ti & 1][i][e] + (float)l[ti & 1][i][e]) + u.f * x[e];
                     if constexpr (kLast) {
                         bf16x8 o;
 #pragma unroll
@@ -326,9 +342,9 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams
                         halfx8 nh, nl;
                         split8(x, nh, nl);
                         *reinterpret_cast<halfx8*>(u.hi2 + at) = nh;
-                        *reinterpret_cast<halfx8*>(u.lo2 + at) = nl;
+                        if (u.lo2) *reinterpret_cast<halfx8*>(u.lo2 + at) = nl;
                     }
-                });
+                }
             }
         });
 }
@@ -394,6 +410,12 @@ __global__ __launch_bounds__(NT) void gram_join_kernel(const float* partial, int
     if (col0 + col < n && row0 + half < n)
         *reinterpret_cast<halfx8*>(S + (col0 + col) * ld + row0 + half) = t;
 }
+
+// Whether X before step i is kept in two halves: what rounding it to one adds in the
+// weak directions grows by a factor up to a in each step left, so the last
+// two steps' X are not (12 times half an FP16 step), which saves a third of the
+// update's traffic there.
+bool two_halves(int i, int steps) { return i == 0 || steps - i > 2; }
 
 unsigned grid_for(int64_t items) {
     const int64_t g = (items + NT - 1) / NT;
@@ -480,20 +502,36 @@ hipError_t gram(const Plan& p, const GemmParams& g, _Float16* S, float f, uint8_
 }
 
 template <In T>
+hipError_t norm(const Call& c, int M, int N, int batch, double* parts, hipStream_t s) {
+    using E = typename InFmt<T>::S;
+    const E* G = static_cast<const E*>(c.G);
+    const bool vec = rows_16b_aligned(G, c.ldg, sizeof(E)) && c.stride_g * sizeof(E) % 16 == 0;
+    hipLaunchKernelGGL(norm_kernel<T>, dim3(kNormParts, batch), dim3(NT), 0, s, G, c.ldg,
+                       c.stride_g, M, N, vec, parts);
+    return hipGetLastError();
+}
+
+template <In T>
 hipError_t init(const Plan& p, const Call& c, _Float16* hi, _Float16* lo, hipStream_t s) {
     using E = typename InFmt<T>::S;
     const E* G = static_cast<const E*>(c.G);
     double* parts = reinterpret_cast<double*>(c.ws + p.parts);
     const bool vec = rows_16b_aligned(G, c.ldg, sizeof(E)) && c.stride_g * sizeof(E) % 16 == 0;
-    hipLaunchKernelGGL(norm_kernel<T>, dim3(kNormParts, p.batch), dim3(NT), 0, s, G, c.ldg,
-                       c.stride_g, p.M, p.N, vec, parts);
+    const hipError_t e = launch_norm(c, p.M, p.N, p.batch, parts, s);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(init_kernel<T>, dim3(grid_for(p.x_size / 8), p.batch), dim3(NT), 0, s, G,
                        c.ldg, c.stride_g, p.M, p.N, vec, parts, (double)c.eps,
-                       std::ldexp(1.0, scale_exp(p)), hi, lo, p.ldx);
+                       std::ldexp(1.0, scale_exp(p.k)), hi, lo, p.ldx);
     return hipGetLastError();
 }
 
 }  // namespace
+
+hipError_t launch_norm(const Call& c, int M, int N, int batch, double* parts, hipStream_t s) {
+    return c.t == In::F32    ? norm<In::F32>(c, M, N, batch, parts, s)
+           : c.t == In::BF16 ? norm<In::BF16>(c, M, N, batch, parts, s)
+                             : norm<In::F16>(c, M, N, batch, parts, s);
+}
 
 hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
     auto half = [&](int64_t at) { return reinterpret_cast<_Float16*>(c.ws + at); };
@@ -504,7 +542,7 @@ hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
                    : c.t == In::BF16 ? init<In::BF16>(p, c, hi[0], lo[0], s)
                                      : init<In::F16>(p, c, hi[0], lo[0], s);
     const bool tall = p.M > p.N;
-    const float xs = std::ldexp(1.0f, scale_exp(p));
+    const float xs = std::ldexp(1.0f, scale_exp(p.k));
     Update u = {};
     u.ldx = p.ldx; u.x_size = p.x_size;
     u.a = c.a; u.f = 1.0f / kPolyScale;
@@ -523,8 +561,8 @@ hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
                                          c.c * (kPolyScale / (kGramScale * kGramScale)),
                                          c.b * (kPolyScale / kGramScale), s);
         if (e != hipSuccess) return e;
-        u.hi = hi[r]; u.lo = lo[r];
-        u.hi2 = hi[w]; u.lo2 = lo[w];
+        u.hi = hi[r]; u.lo = two_halves(i, c.steps) ? lo[r] : nullptr;
+        u.hi2 = hi[w]; u.lo2 = two_halves(i + 1, c.steps) ? lo[w] : nullptr;
         const bool last = i + 1 == c.steps;
         if (tall) {
             g = operands(p, p.M, p.N, p.n, hi[r], p.ldx, p.x_size, B, p.lds, p.s_size);

@@ -2,6 +2,8 @@
 // point (orth_api.cpp) and the kernels (k_orth.hip).
 #pragma once
 
+#include <cmath>
+
 #include "gemm_common.hpp"
 
 namespace dgt {
@@ -22,6 +24,51 @@ struct Plan {
     int splits, kc;
     int64_t hi[2], lo[2], gram, poly, partial, parts, bytes;
 };
+
+// Small matrices (k_orth_small.hip): every matrix padded with zeros to
+// multiples of 64 in both dimensions, X held both ways round.
+struct SmallPlan {
+    int M, N, batch, n, k;      // n <= k: a tall G is taken transposed
+    int n64, k64;
+    int64_t x_size, s_size;     // elements of one matrix
+    int64_t x[2], xt[2], lo[2], gram, poly, parts, bytes;
+};
+
+// Whether a call takes them: products whose 32 x 32 tiles, a workgroup each,
+// make three rounds of the compute units at most.  Measured, us (these / the tile
+// kernels): 64^2 45 / 81, 256^2 59 / 128, 512^2 84 / 164, 768^2 192 / 207, 1024^2 286 / 233,
+// 256 x 1024 76 / 148, 256 x 4096 165 / 164, 4 x 256^2 68 / 131, 16 x 256^2 136 / 127.
+inline bool is_small(int M, int N, int batch) {
+    const int64_t n = ((M < N ? M : N) + 63ll) / 64 * 64, k = ((M < N ? N : M) + 63ll) / 64 * 64;
+    return k <= 2048 && n * k / 1024 * batch <= 800;
+}
+
+inline SmallPlan make_small_plan(int M, int N, int batch) {
+    SmallPlan p;
+    p.M = M; p.N = N; p.batch = batch;
+    p.n = M < N ? M : N;
+    p.k = M < N ? N : M;
+    p.n64 = (p.n + 63) / 64 * 64;
+    p.k64 = (p.k + 63) / 64 * 64;
+    p.x_size = (int64_t)p.n64 * p.k64;
+    p.s_size = (int64_t)p.n64 * p.n64;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    p.parts = take((int64_t)batch * kNormParts * 8);
+    for (int i = 0; i < 2; ++i) {
+        p.x[i] = take(batch * p.x_size * 2);
+        p.xt[i] = take(batch * p.x_size * 2);
+        p.lo[i] = take(batch * p.x_size * 2);
+    }
+    p.gram = take(batch * p.s_size * 2);
+    p.poly = take(batch * p.s_size * 2);
+    p.bytes = at;
+    return p;
+}
 
 constexpr int kGramTile = 128;  // of a Gram matrix in parts
 
@@ -79,7 +126,20 @@ struct Call {
     uint8_t* ws;
 };
 
+inline int64_t workspace_bytes(int M, int N, int batch) {
+    return is_small(M, N, batch) ? make_small_plan(M, N, batch).bytes : make_plan(M, N, batch).bytes;
+}
+
 hipError_t launch(const Plan& p, const Call& c, hipStream_t s);
+hipError_t launch_small(const SmallPlan& p, const Call& c, hipStream_t s);
+// The partial sums of squares of a batch (k_orth.hip).
+hipError_t launch_norm(const Call& c, int M, int N, int batch, double* parts, hipStream_t s);
+
+// FP16's range: S is held times 2^12, the step polynomial times 2^10, X times
+// 2^scale_exp near the square root of its larger dimension.
+constexpr float kGramScale = 4096.0f;
+constexpr float kPolyScale = 1024.0f;
+inline int scale_exp(int k) { return (int)std::lround(0.5 * std::log2((double)k)); }
 
 }  // namespace orth
 }  // namespace dgt

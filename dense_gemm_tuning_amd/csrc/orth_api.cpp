@@ -31,7 +31,7 @@ int64_t gemm_orthogonalize_workspace_size(int M, int N, int batch) {
     if (batch < 0 || batch > kMaxBatch) return GEMM_ERR_ARG;
     if (M < 0 || N < 0 || too_large(M, N, batch)) return GEMM_ERR_DIM;
     if (M == 0 || N == 0 || batch == 0) return 0;
-    return orth::make_plan(M, N, batch).bytes;
+    return orth::workspace_bytes(M, N, batch);
 }
 
 int gemm_orthogonalize(int dtype, int M, int N, const void* G, int ldg, int64_t stride_g,
@@ -47,14 +47,14 @@ int gemm_orthogonalize(int dtype, int M, int N, const void* G, int ldg, int64_t 
     if (ldg < std::max(1, N) || ldo < std::max(1, N)) return GEMM_ERR_LD;
     if (M == 0 || N == 0 || batch == 0) return GEMM_OK;
     if (G == nullptr || O == nullptr) return GEMM_ERR_NULL;
-    const orth::Plan plan = orth::make_plan(M, N, batch);
-    if (workspace == nullptr || workspace_bytes < plan.bytes) return GEMM_ERR_WORKSPACE;
+    const int64_t need = orth::workspace_bytes(M, N, batch);
+    if (workspace == nullptr || workspace_bytes < need) return GEMM_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return GEMM_ERR_ALIGN;
     const int esz = elem_size(t);
     const uint64_t o_span = span_bytes(M, N, ldo, 2);
     // the problems of a batch must not write over each other
     if (batch > 1 && (uint64_t)stride_o * 2 < o_span) return GEMM_ERR_OVERLAP;
-    const Range rw = batch_range(workspace, (uint64_t)plan.bytes, 0, 1);
+    const Range rw = batch_range(workspace, (uint64_t)need, 0, 1);
     if (overlaps(rw, batch_range(G, span_bytes(M, N, ldg, esz), stride_g * esz, batch)) ||
         overlaps(rw, batch_range(O, o_span, stride_o * 2, batch)))
         return GEMM_ERR_OVERLAP;
@@ -65,7 +65,10 @@ int gemm_orthogonalize(int dtype, int M, int N, const void* G, int ldg, int64_t 
     call.steps = steps;
     call.a = a; call.b = b; call.c = c; call.eps = eps;
     call.ws = static_cast<uint8_t*>(workspace);
-    const hipError_t e = orth::launch(plan, call, static_cast<hipStream_t>(stream));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = orth::is_small(M, N, batch)
+                             ? orth::launch_small(orth::make_small_plan(M, N, batch), call, s)
+                             : orth::launch(orth::make_plan(M, N, batch), call, s);
     if (e == hipErrorInvalidConfiguration) return GEMM_ERR_DIM;  // more tiles than a grid holds
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
