@@ -59,9 +59,9 @@ __device__ __forceinline__ void load8(const typename InFmt<T>::S* row, int col, 
     }
 }
 
-// kNormParts partial sums of squares per matrix, in 64 bits (an fp32 input's
-// squares leave fp32's range): workgroup x of matrix blockIdx.y takes every
-// kNormParts-th run of 8 * NT elements.  The order is fixed.
+// Partial sums of squares per matrix, in 64 bits (an fp32 input's squares
+// leave fp32's range): workgroup x of matrix blockIdx.y takes every
+// gridDim.x-th run of 8 * NT elements.  The order is fixed.
 template <In T>
 __global__ __launch_bounds__(NT) void norm_kernel(const typename InFmt<T>::S* G, int64_t ldg,
                                                   int64_t stride, int M, int N, bool vec,
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const typename InFmt<T>::S* G,
     const int64_t total = (int64_t)M * per_row;
     double sum = 0.0;
     for (int64_t e = (int64_t)blockIdx.x * NT + threadIdx.x; e < total;
-         e += (int64_t)kNormParts * NT) {
+         e += (int64_t)gridDim.x * NT) {
         float v[8];
         load8<T>(G + e / per_row * ldg, (int)(e % per_row) * 8, N, vec, v);
 #pragma unroll
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const typename InFmt<T>::S* G,
         if ((int)threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
         __syncthreads();
     }
-    if (threadIdx.x == 0) parts[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = red[0];
+    if (threadIdx.x == 0) parts[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = red[0];
 }
 
 // Eight values as two FP16 halves, x = hi + lo to 22 bits.
@@ -100,15 +100,16 @@ __device__ __forceinline__ void split8(const float (&x)[8], halfx8& hi, halfx8& 
 template <In T>
 __global__ __launch_bounds__(NT) void init_kernel(const typename InFmt<T>::S* G, int64_t ldg,
                                                   int64_t stride, int M, int N, bool vec,
-                                                  const double* parts, double eps, double scale,
-                                                  _Float16* hi, _Float16* lo, int64_t ldx) {
-    static_assert(kNormParts == NT, "one partial sum per lane");
+                                                  const double* parts, int nparts, double eps,
+                                                  double scale, _Float16* hi, _Float16* lo, int64_t ldx) {
     const int64_t z = blockIdx.y;
     G += z * stride;
     hi += z * M * ldx;
     lo += z * M * ldx;
     __shared__ double red[NT];
-    red[threadIdx.x] = parts[z * kNormParts + threadIdx.x];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < nparts; i += NT) sum += parts[z * nparts + i];
+    red[threadIdx.x] = sum;
     __syncthreads();
     for (int h = NT / 2; h > 0; h /= 2) {
         if ((int)threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
@@ -506,7 +507,7 @@ hipError_t norm(const Call& c, int M, int N, int batch, double* parts, hipStream
     using E = typename InFmt<T>::S;
     const E* G = static_cast<const E*>(c.G);
     const bool vec = rows_16b_aligned(G, c.ldg, sizeof(E)) && c.stride_g * sizeof(E) % 16 == 0;
-    hipLaunchKernelGGL(norm_kernel<T>, dim3(kNormParts, batch), dim3(NT), 0, s, G, c.ldg,
+    hipLaunchKernelGGL(norm_kernel<T>, dim3(norm_parts(M, N), batch), dim3(NT), 0, s, G, c.ldg,
                        c.stride_g, M, N, vec, parts);
     return hipGetLastError();
 }
@@ -520,7 +521,7 @@ hipError_t init(const Plan& p, const Call& c, _Float16* hi, _Float16* lo, hipStr
     const hipError_t e = launch_norm(c, p.M, p.N, p.batch, parts, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(init_kernel<T>, dim3(grid_for(p.x_size / 8), p.batch), dim3(NT), 0, s, G,
-                       c.ldg, c.stride_g, p.M, p.N, vec, parts, (double)c.eps,
+                       c.ldg, c.stride_g, p.M, p.N, vec, parts, norm_parts(p.M, p.N), (double)c.eps,
                        std::ldexp(1.0, scale_exp(p.k)), hi, lo, p.ldx);
     return hipGetLastError();
 }

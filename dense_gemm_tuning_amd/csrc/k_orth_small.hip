@@ -31,17 +31,18 @@ typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
 template <In E, bool kTall>
 __global__ __launch_bounds__(NTI) void small_init_kernel(const typename InFmt<E>::S* G, int64_t ldg,
                                                          int64_t stride, SmallPlan p,
-                                                         const double* parts, double eps,
+                                                         const double* parts, int nparts, double eps,
                                                          double scale, _Float16* x, _Float16* xt,
                                                          _Float16* lo) {
-    static_assert(kNormParts == NTI, "one partial sum per lane");
     const int64_t z = blockIdx.y;
     G += z * stride;
     x += z * p.x_size;
     xt += z * p.x_size;
     lo += z * p.x_size;
     __shared__ double red[NTI];
-    red[threadIdx.x] = parts[z * kNormParts + threadIdx.x];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < nparts; i += NTI) sum += parts[z * nparts + i];
+    red[threadIdx.x] = sum;
     __syncthreads();
     for (int h = NTI / 2; h > 0; h /= 2) {
         if ((int)threadIdx.x < h) red[threadIdx.x] += red[threadIdx.x + h];
@@ -184,7 +185,7 @@ hipError_t init(const SmallPlan& p, const Call& c, const double* parts, _Float16
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(NTI), 0, s,
                            static_cast<const typename InFmt<E>::S*>(c.G), c.ldg, c.stride_g, p, parts,
-                           (double)c.eps, std::ldexp(1.0, scale_exp(p.k)), x, xt, lo);
+                           norm_parts(p.M, p.N), (double)c.eps, std::ldexp(1.0, scale_exp(p.k)), x, xt, lo);
         return hipGetLastError();
     };
     return p.M > p.N ? go(small_init_kernel<E, true>) : go(small_init_kernel<E, false>);
