@@ -62,9 +62,8 @@ struct ScaleCopy {
 };
 
 template <int R, bool kEdge, bool kTail>
-__global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p, int tiles_m,
-                                                                      int tiles_n, int nb,
-                                                                      int grouped) {
+__global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p, int tiles_n,
+                                                                      int nb) {
     constexpr int TM = Geo<R>::TM;
     using Op = KcOperand<R>;
     constexpr int CKC = Op::kHalfCopies;
@@ -78,8 +77,10 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1, h = lane >> 5;
-    const TileIdx tile = xcd_tile(tiles_m, tiles_n, grouped != 0);
-    const int m0 = tile.bm * R, n0 = tile.bn * R;
+    // tile rows in order: as for the 16-bit kernel with both operands
+    // k-contiguous, XCD-grouped tiles measured 3% slower (8192^3)
+    const unsigned bm = blockIdx.x / (unsigned)tiles_n;
+    const int m0 = (int)bm * R, n0 = (int)(blockIdx.x - bm * (unsigned)tiles_n) * R;
     const int ku = 8 * nb;                  // row length in 16-bit units
     const int nk = (ku + BK - 1) / BK;      // slices of four blocks
     const int groups = (nb + 15) / 16;
@@ -251,45 +252,99 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
     DMA_WAIT_VMCNT(0);  // no copy may still target LDS when the workgroup ends
 
     // Accumulator layout: register r of lane l is row 8*(r/4) + 4*(l/32) +
-    // r%4, column l%32 of the MFMA tile.  Stores are non-temporal, and with
-    // beta != 0 C is read one MFMA tile ahead of its stores, as in the 16-bit kernel.
-    const int col0 = n0 + wn * (R / 2) + (lane & 31);
-    const int row0 = m0 + wm * (R / 2) + 4 * h;
-    float* cbase = p.C + (int64_t)row0 * p.ldc + col0;
+    // r%4, column l%32 of the MFMA tile.
     const float alpha = p.alpha, beta = p.beta;
-    float bias[TM];
+    if constexpr (kEdge) {
+        // A wave's rows of MFMA tiles through LDS, then row by row in a short
+        // loop: guarded element by element in straight code, the stores of an
+        // edge tile are several KiB of instructions fetched once, 6.5 us of a 12 us
+        // product of 1000 x 1000 x 1000.  Column c of row r sits at c ^ 32*(r/4 & 1).
+        constexpr int W = R / 2;
+        dma::barrier();  // no wave still reads the stages
+        float* mem = reinterpret_cast<float*>((wave < 2 ? sA0 : sA1) + (wave & 1) * (Op::kStage / 2));
+        static_assert(32 * W * 4 <= Op::kStage / 2, "a wave's region holds 32 rows");
+        const int row0 = m0 + wm * W, col0 = n0 + wn * W + lane;
+        float bias[W / 64];
 #pragma unroll
-    for (int tj = 0; tj < TM; ++tj)
-        bias[tj] = p.bias && (!kEdge || col0 + tj * 32 < p.N) ? p.bias[col0 + tj * 32] : -0.0f;
-    auto ok = [&](int ti, int tj, int r) {
-        return !kEdge || (row0 + ti * 32 + 8 * (r >> 2) + (r & 3) < p.M && col0 + tj * 32 < p.N);
-    };
-    auto at = [&](int ti, int tj, int r) -> float* {
-        return &cbase[(int64_t)(ti * 32 + 8 * (r >> 2) + (r & 3)) * p.ldc + tj * 32];
-    };
-    if (beta == 0.0f) {
+        for (int c = 0; c < W / 64; ++c)
+            bias[c] = p.bias && col0 + 64 * c < p.N ? p.bias[col0 + 64 * c] : -0.0f;
 #pragma unroll
-        for (int ti = 0; ti < TM; ++ti)
+        for (int ti = 0; ti < TM; ++ti) {
+            asm volatile("" ::: "memory");  // LDS keeps the wave's order, so must the compiler
 #pragma unroll
             for (int tj = 0; tj < TM; ++tj)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (ok(ti, tj, r))
-                        __builtin_nontemporal_store(alpha * acc[ti][tj][r] + bias[tj], at(ti, tj, r));
+                    mem[(8 * (r >> 2) + 4 * h + (r & 3)) * W + ((tj * 32 + (lane & 31)) ^ (32 * h))] =
+                        acc[ti][tj][r];
+            asm volatile("" ::: "memory");
+            const int rows = min(32, p.M - (row0 + 32 * ti));
+            float* crow = p.C + (int64_t)(row0 + 32 * ti) * p.ldc + col0;
+            // Whole batches of rows without a guard but the column's; C is read
+            // (beta != 0) a batch ahead of its stores: vector memory operations
+            // complete in order, so a read waits for the stores before it.
+            constexpr int B = 8;
+            auto store_rows = [&](auto bc) DGT_INLINE {
+                constexpr bool kBeta = decltype(bc)::value;
+                auto put = [&](int r0, auto nc) DGT_INLINE {
+                    constexpr int n = decltype(nc)::value;
+#pragma unroll
+                    for (int c = 0; c < W / 64; ++c) {
+                        if (col0 + 64 * c >= p.N) continue;
+                        float* at = crow + (int64_t)r0 * p.ldc + 64 * c;
+                        float x[n], o[n];
+#pragma unroll
+                        for (int r = 0; r < n; ++r) {
+                            const int row = r0 + r;
+                            x[r] = alpha * mem[row * W + ((lane + 64 * c) ^ (32 * ((row >> 2) & 1)))];
+                            o[r] = kBeta ? beta * at[(int64_t)r * p.ldc] : 0.0f;
+                        }
+#pragma unroll
+                        for (int r = 0; r < n; ++r)
+                            __builtin_nontemporal_store((kBeta ? x[r] + o[r] : x[r]) + bias[c],
+                                                        &at[(int64_t)r * p.ldc]);
+                    }
+                };
+                int r0 = 0;
+                for (; r0 + B <= rows; r0 += B) put(r0, std::integral_constant<int, B>{});
+                for (; r0 < rows; ++r0) put(r0, std::integral_constant<int, 1>{});
+            };
+            if (beta == 0.0f) store_rows(std::false_type{});
+            else store_rows(std::true_type{});
+        }
     } else {
+        // Stores are non-temporal, and with beta != 0 C is read one MFMA tile
+        // ahead of its stores, as in the 16-bit kernel.
+        const int col0 = n0 + wn * (R / 2) + (lane & 31);
+        float* cbase = p.C + (int64_t)(m0 + wm * (R / 2) + 4 * h) * p.ldc + col0;
+        float bias[TM];
 #pragma unroll
-        for (int ti = 0; ti < TM; ++ti)
+        for (int tj = 0; tj < TM; ++tj) bias[tj] = p.bias ? p.bias[col0 + tj * 32] : -0.0f;
+        auto at = [&](int ti, int tj, int r) -> float* {
+            return &cbase[(int64_t)(ti * 32 + 8 * (r >> 2) + (r & 3)) * p.ldc + tj * 32];
+        };
+        if (beta == 0.0f) {
 #pragma unroll
-            for (int tj = 0; tj < TM; ++tj) {
-                float cv[16];
+            for (int ti = 0; ti < TM; ++ti)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) cv[r] = ok(ti, tj, r) ? *at(ti, tj, r) : 0.0f;
+                for (int tj = 0; tj < TM; ++tj)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (ok(ti, tj, r))
+                    for (int r = 0; r < 16; ++r)
+                        __builtin_nontemporal_store(alpha * acc[ti][tj][r] + bias[tj], at(ti, tj, r));
+        } else {
+#pragma unroll
+            for (int ti = 0; ti < TM; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < TM; ++tj) {
+                    float cv[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) cv[r] = *at(ti, tj, r);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
                         __builtin_nontemporal_store(
                             (alpha * acc[ti][tj][r] + beta * cv[r]) + bias[tj], at(ti, tj, r));
-            }
+                }
+        }
     }
 }
 
@@ -299,7 +354,7 @@ hipError_t launch_tiles(const Params& p, hipStream_t s) {
     const int64_t wgs = (int64_t)tiles_m * tiles_n;
     if (wgs > 0x7fffffff) return hipErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, s, p, tiles_m, tiles_n, nb, 0);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, s, p, tiles_n, nb);
         return hipGetLastError();
     };
     if (nb % 16 != 0) return go(mx4_tile_kernel<R, true, true>);
