@@ -667,11 +667,12 @@ def gemm_quantized(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=
     if M == 0 or N == 0:
         return GEMM_OK
     if SA is None:
-        return _call_on(index, stream, _load().gemm_mx4_a16, dtype, M, N, K, alpha, A.data_ptr(),
-                        lda, B.data_ptr(), ldb, SB.data_ptr(), ldsb, beta, C.data_ptr(), ldc,
+        return _call_on(index, stream, _load().gemm_mx4_a16, dtype, M, N, K, float(alpha),
+                        A.data_ptr(), lda, B.data_ptr(), ldb, SB.data_ptr(), ldsb, float(beta),
+                        C.data_ptr(), ldc,
                         bias_ptr)
-    return _call_on(index, stream, _load().gemm_mx4, M, N, K, alpha, A.data_ptr(), lda,
-                    SA.data_ptr(), ldsa, B.data_ptr(), ldb, SB.data_ptr(), ldsb, beta,
+    return _call_on(index, stream, _load().gemm_mx4, M, N, K, float(alpha), A.data_ptr(), lda,
+                    SA.data_ptr(), ldsa, B.data_ptr(), ldb, SB.data_ptr(), ldsb, float(beta),
                     C.data_ptr(), ldc, bias_ptr)
 
 
@@ -719,7 +720,7 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
                   else torch.cuda.ExternalStream(stream, device=O.device))
             with torch.cuda.stream(on):
                 workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
-    a, b, c = coefficients
+    a, b, c = (float(x) for x in coefficients)
     return _call_on(index, stream, _load().gemm_orthogonalize, dtype, M, N, G2.data_ptr(), _ld(G2),
-                    sg, O2.data_ptr(), _ld(O2), so, batch, steps, a, b, c, eps,
+                    sg, O2.data_ptr(), _ld(O2), so, batch, int(steps), a, b, c, float(eps),
                     workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -53,13 +53,6 @@ __device__ __forceinline__ float epilogue(float acc, const Params& p, const floa
 // (they take the exponent field alone).
 __device__ __forceinline__ float scale_bits(uint32_t s) { return __uint_as_float(s << 23); }
 
-// Scale byte s as the number it stands for.
-__device__ __forceinline__ float scale_value(uint32_t s) {
-    return s == 0 ? __uint_as_float(0x00400000u)            // 2^-127
-           : s == 255 ? __uint_as_float(0x7fc00000u)        // NaN
-                      : __uint_as_float(s << 23);
-}
-
 hipError_t launch_quantize(In t, bool trans, int M, int K, const void* X, int64_t ldx, uint8_t* Q,
                            int64_t ldq, uint8_t* S, int64_t lds, hipStream_t s);
 hipError_t launch_dequantize(In t, int M, int K, const uint8_t* Q, int64_t ldq, const uint8_t* S,

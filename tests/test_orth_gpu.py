@@ -192,3 +192,96 @@ def test_update_then_serve():
     w = mp.values(*mp.quantize(W.double().cpu().numpy()), I)
     d = D.double().cpu().numpy()
     assert (np.abs(Y.double().cpu().numpy() - d @ w.T) <= (I + 4) * 2.0 ** -23 * (np.abs(d) @ np.abs(w).T)).all()
+
+
+# The tests above run matrices small enough for 32 x 32 tiles; these sizes
+# take the large tiles: edges in both dimensions, K tails, a long k summed in
+# parts, and a few rows or columns only.
+LARGE = [(1100, 900), (900, 2100), (2100, 260), (260, 2100), (1030, 1030), (1, 2300), (2305, 3), (2304, 130)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N", LARGE)
+def test_large_one_step_within_its_rounding_bound(M, N, dtype):
+    say("orth large step", M, N, dtype)
+    G = matrix(np.random.default_rng([M, N, 3]), M, N, dtype)
+    O = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dgt.check(dgt.orthogonalize(G.cuda(), O, steps=1, coefficients=COEF))
+    g = G.double().numpy()
+    err = np.abs(O.double().cpu().numpy() - mp.newton_schulz(g, 1, *COEF, 1e-7))
+    bound = mp.newton_schulz_step_bound(g, *COEF, 1e-7)
+    assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("kind", ["normal", "lowrank"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", LARGE)
+def test_large_five_steps(M, N, dtype, kind):
+    G = matrix(np.random.default_rng([M, N, 4]), M, N, dtype, kind)
+    O = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dgt.check(dgt.orthogonalize(G.cuda(), O))
+    want = mp.newton_schulz(G.double().numpy(), 5, *COEF, 1e-7)
+    rel = np.linalg.norm(O.double().cpu().numpy() - want) / np.linalg.norm(want)
+    say("orth large", M, N, dtype, kind, "normwise", rel)
+    assert rel <= NORMWISE
+
+
+@pytest.mark.parametrize("M,N", [(950, 1000), (1000, 940), (260, 2100), (2100, 130)])
+def test_large_batch_strides_and_guards(M, N):
+    """Padded rows and problem strides, results off 16-byte rows, a workspace
+    that starts as NaN: every problem right, nothing else written, and a NaN
+    in one problem stays there."""
+    nb = 3
+    rng = np.random.default_rng([M, N, 5])
+    gp, op = N + 3, N + 5
+    gs, os_ = M * gp + 11, M * op + 9
+    Gf = torch.full((nb * gs,), float("nan"), device="cuda")
+    Of = torch.full((nb * os_ + 1,), -7.0, dtype=torch.bfloat16, device="cuda")
+    G = Gf.as_strided((nb, M, N), (gs, gp, 1))
+    O = Of[1:].as_strided((nb, M, N), (os_, op, 1))
+    for z in range(nb):
+        G[z] = matrix(rng, M, N, "f32").cuda()
+    need = dgt.gemm_orthogonalize_workspace_size(M, N, nb)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    dgt.check(dgt.orthogonalize(G, O, workspace=ws[:need]))
+    for z in range(nb):
+        want = mp.newton_schulz(G[z].double().cpu().numpy(), 5, *COEF, 1e-7)
+        rel = np.linalg.norm(O[z].double().cpu().numpy() - want) / np.linalg.norm(want)
+        assert rel <= NORMWISE
+    guard = torch.ones(nb * os_ + 1, dtype=torch.bool)
+    guard[1:].as_strided((nb, M, N), (os_, op, 1)).fill_(False)
+    assert (Of.cpu()[guard] == -7.0).all()
+    assert (ws[need:] == 0xFF).all()
+    base = O.clone()
+    G[1, M // 2, N // 2] = float("nan")
+    dgt.check(dgt.orthogonalize(G, O, workspace=ws[:need]))
+    assert torch.isnan(O[1]).all()
+    assert torch.equal(O[0], base[0]) and torch.equal(O[2], base[2])
+
+
+@pytest.mark.parametrize("M,N", [(2200, 300), (1000, 1100)])
+def test_large_in_place_and_replayed(M, N):
+    """The result over its input; captured and replayed on new inputs."""
+    rng = np.random.default_rng([M, N, 6])
+    G = matrix(rng, M, N, "bf16").cuda()
+    O = torch.empty_like(G)
+    ws = torch.empty(dgt.gemm_orthogonalize_workspace_size(M, N, 1), dtype=torch.uint8, device="cuda")
+    dgt.check(dgt.orthogonalize(G, O, workspace=ws))
+    H = G.clone()
+    dgt.check(dgt.orthogonalize(H, H, workspace=ws))
+    assert torch.equal(H, O)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dgt.check(dgt.orthogonalize(G, O, workspace=ws))
+    for _ in range(3):
+        G.copy_(matrix(rng, M, N, "bf16"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = O.clone()
+        O.zero_()
+        dgt.check(dgt.orthogonalize(G, O, workspace=ws))
+        torch.cuda.synchronize()
+        assert torch.equal(got, O)
+    dgt.check(dgt.orthogonalize(torch.zeros_like(G), O, workspace=ws))
+    assert not O.any()
