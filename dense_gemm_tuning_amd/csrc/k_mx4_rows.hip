@@ -366,23 +366,52 @@ bool rows_copyable(const Params& p) {
     return rows_16b_aligned(p.A, p.lda, 2) && p.lda < kMaxBufferPitch;
 }
 
-}  // namespace
-
-// This kernel or the wave-private one, us on K = 8192 (wave-private / this):
-//   MX4   M = 8:  N = 3584 7.3 / 12.4, 8192 10.9 / 12.8, 14336 16.3 / 14.3
-//         M = 32: 11.5 / 15.6, 15.5 / 16.3, 22.1 / 17.6;  M = 64: 19.5 / 16.5, 24.5 / 17.2
-//   BF16  M = 8:  12.2 / 21.7, 16.1 / 22.2, 20.0 / 23.0, 28672 37.9 / 30.8
-//         M = 32: 24.0 / 24.8, 28.4 / 25.4;  M = 64: 26.8 / 29.7, 33.6 / 30.4, 64 / 31.5
-//   FP16  M = 8:  11.4 / 31.6, 15.9 / 32.2, 27.0 / 33.2; M = 64: 25.2 / 36.7, 48.6 / 37.9
-hipError_t launch_product(const Params& p, hipStream_t s) {
-    if (p.M <= 32 && p.N <= 8192) return launch_skinny(p, s);
-    if (p.M <= 16) return launch_width<Kind::MX4, 1, 4, 3>(p, s);
-    if (p.M <= 32) return launch_width<Kind::MX4, 2, 4, 3>(p, s);
-    return launch_width<Kind::MX4, 4, 4, 3>(p, s);
+// Workgroups of a launch in strips of `cols` columns and rb blocks of 16 rows,
+// and whether the CUs take them in one round.
+bool one_round(const Params& p, int cols, int rb) {
+    return ((int64_t)p.N + cols - 1) / cols * (((int64_t)p.M + 16 * rb - 1) / (16 * rb)) <= dma::kCUs;
 }
 
+}  // namespace
+
+// Few outputs leave only K to share: the form with the smallest workgroups
+// (16 rows x 16, then 32 columns, wave-private) whose launch is one round of
+// the CUs has the shortest way through K; then 32 x 32, and one round of this
+// kernel, where K is long or M small.  Else tiles above 64 rows.  us (16 x 16 / 16 x 32
+// / 32 x 32 wave-private, this kernel, tiles), weights in L2:
+//   K = 8192: M = 32   N = 2048   6.8   8.3  11.8        14.7
+//                      N = 8192  22.7  17.3  13.3  16.3  21.3
+//             M = 128  N = 1024  11.4   8.1  11.5  12.2  14.5
+//                      N = 2048  20.5  15.1  11.6  12.4  14.6
+//                      N = 4096  40.7  30.6  23.8  12.9  14.7
+//                      N = 8192  79.8  60.5  46.7  15.9  21.9
+//   K = 1024: M = 128  N = 1024   4.3   4.4   4.3   5.5   4.6
+//                      N = 4096  10.1   9.5   7.6   5.6   4.7
+// and from memory M = 8, K = 8192: N = 3584 7.3 (16 x 16) / 12.4 (this), 8192 10.9
+// (16 x 32) / 12.8, 14336 18.7 / 14.3.
+hipError_t launch_product(const Params& p, hipStream_t s) {
+    if (one_round(p, 16, 1)) return launch_skinny(p, 1, 16, s);
+    if (one_round(p, 32, 1)) return launch_skinny(p, 1, 32, s);
+    const bool long_k = p.K >= 4096;
+    if (p.M > 16 && (p.M <= 64 || long_k) && one_round(p, 32, 2)) return launch_skinny(p, 2, 32, s);
+    if (p.M <= 16) return launch_width<Kind::MX4, 1, 4, 3>(p, s);
+    if (p.M <= 32) return launch_width<Kind::MX4, 2, 4, 3>(p, s);
+    if (p.M <= 64 || (long_k && one_round(p, 64, 4))) return launch_width<Kind::MX4, 4, 4, 3>(p, s);
+    return launch_product_tile(p, s);
+}
+
+// The same for 16-bit A, up to 512 rows (a strip's A comes from L2 only while other
+// strips read it too).  us at K = 8192, weights in L2 (wave-private / this):
+//   BF16  M = 32:  N = 1024 13.6 / 18.7, 4096 16.9 / 19.7
+//         M = 64:  14.3 / 26.5, 19.8 / 26.6;  M = 256: N = 1024 20.2 / 29.0
+//         M = 1024: N = 256 41.5 / 29.9
+//   FP16  M = 32:  12.6 / 23.0, 15.9 / 23.1;  M = 64: 12.8 / 32.6, 24.7 / 33.7
+// and from memory, M = 8: BF16 N = 14336 20.0 / 23.0, 28672 37.9 / 30.8; FP16
+// 14336 27.0 / 33.2.
 hipError_t launch_product16(In t, const Params& p, hipStream_t s) {
-    if (!rows_copyable(p) || (p.M <= 16 && p.N <= 14336)) return launch_skinny16(t, p, s);
+    for (int cols = 16; cols <= 64 && p.M <= 512; cols *= 2)
+        if (one_round(p, cols, 1)) return launch_skinny16(t, p, 1, cols, s);
+    if (!rows_copyable(p)) return launch_skinny16(t, p, t == In::BF16 && p.M > 16 ? 2 : 1, 64, s);
     if (t == In::F16)
         return p.M <= 16   ? launch_width<Kind::F16, 1, 4, 4>(p, s)
                : p.M <= 32 ? launch_width<Kind::F16, 2, 4, 4>(p, s)

@@ -1,10 +1,10 @@
-// k_mx4_skinny.hip -- decode-shaped products with a microscaled 4-bit weight
-// of few columns (a share of a layer): few rows of A (MX4, BF16 or FP16, k
-// contiguous) against B stored N x K.  As for the library's other skinny
-// kernels the time is the time to stream B once, here 17 bytes per 32 weights,
-// and with few columns the latency of one pass: narrow strips, K split over
-// the waves.  Wide weights and most batches of more than 16 rows take
-// k_mx4_rows.hip (the choice is made there).
+// k_mx4_skinny.hip -- products of few outputs with a microscaled 4-bit weight
+// (decode batches against a share of a layer, short batches against narrow
+// weights): A (MX4, BF16 or FP16, k contiguous) against B stored N x K.  The
+// time is the latency of one pass through K (and, of a weight that comes from
+// memory, of its 17 bytes per 32 elements): narrow strips, few rows, K split over the
+// waves.  Wide weights and larger batches take k_mx4_rows.hip, where the choice
+// is made, or tiles.
 //
 // Each wave copies its pieces of B straight into a private LDS ring by
 // buffer loads that write LDS (no workgroup barrier in the loop; the scheme of
@@ -414,30 +414,28 @@ hipError_t launch_cfg(const Params& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Strip width: the narrowest whose workgroups take one round of the CUs.  At
-// K = 8192, MX4, M = 8, us for 16 / 32 / 64 columns: N = 3584 7.3 / 8.9 / 12.4,
-// 8192 12.0 / 10.9 / 13.5, 14336 20.4 / 18.7 / 16.3.
-template <Kind KA, int RB, int ROWB, int NS>
-hipError_t launch_strip(const Params& p, hipStream_t s) {
-    const int64_t chunks = (p.M + 16 * RB - 1) / (16 * RB);
-    auto fits = [&](int cols) { return ((int64_t)p.N + cols - 1) / cols * chunks <= dma::kCUs; };
-    if (fits(16)) return launch_cfg<KA, RB, ROWB, NS, 1, 16>(p, s);
-    if (fits(32)) return launch_cfg<KA, RB, ROWB, NS, 1, 32>(p, s);
-    return launch_cfg<KA, RB, ROWB, NS, 2, 32>(p, s);
-}
-
 }  // namespace
 
-// M <= 32.
-hipError_t launch_skinny(const Params& p, hipStream_t s) {
-    return p.M <= 16 ? launch_strip<Kind::MX4, 1, 256, 2>(p, s)
-                     : launch_strip<Kind::MX4, 2, 256, 2>(p, s);
+// The forms that the choice in k_mx4_rows.hip reaches: rb blocks of 16 rows,
+// strips of `cols` columns.
+hipError_t launch_skinny(const Params& p, int rb, int cols, hipStream_t s) {
+    if (rb == 1 && cols == 16) return launch_cfg<Kind::MX4, 1, 256, 2, 1, 16>(p, s);
+    if (rb == 1 && cols == 32) return launch_cfg<Kind::MX4, 1, 256, 2, 1, 32>(p, s);
+    if (rb == 2 && cols == 32) return launch_cfg<Kind::MX4, 2, 256, 2, 1, 32>(p, s);
+    return hipErrorInvalidConfiguration;
 }
 
-hipError_t launch_skinny16(In t, const Params& p, hipStream_t s) {
-    if (t == In::F16) return launch_strip<Kind::F16, 1, 128, 4>(p, s);
-    return p.M <= 16 ? launch_strip<Kind::BF16, 1, 256, 2>(p, s)
-                     : launch_strip<Kind::BF16, 2, 128, 4>(p, s);
+hipError_t launch_skinny16(In t, const Params& p, int rb, int cols, hipStream_t s) {
+    if (t == In::F16 && rb == 1)
+        return cols == 16   ? launch_cfg<Kind::F16, 1, 128, 4, 1, 16>(p, s)
+               : cols == 32 ? launch_cfg<Kind::F16, 1, 128, 4, 1, 32>(p, s)
+                            : launch_cfg<Kind::F16, 1, 128, 4, 2, 32>(p, s);
+    if (t == In::BF16 && rb == 1)
+        return cols == 16   ? launch_cfg<Kind::BF16, 1, 256, 2, 1, 16>(p, s)
+               : cols == 32 ? launch_cfg<Kind::BF16, 1, 256, 2, 1, 32>(p, s)
+                            : launch_cfg<Kind::BF16, 1, 256, 2, 2, 32>(p, s);
+    if (t == In::BF16 && rb == 2) return launch_cfg<Kind::BF16, 2, 128, 4, 2, 32>(p, s);
+    return hipErrorInvalidConfiguration;
 }
 
 }  // namespace mx4

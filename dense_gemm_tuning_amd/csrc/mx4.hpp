@@ -57,12 +57,13 @@ hipError_t launch_quantize(In t, bool trans, int M, int K, const void* X, int64_
                            int64_t ldq, uint8_t* S, int64_t lds, hipStream_t s);
 hipError_t launch_dequantize(In t, int M, int K, const uint8_t* Q, int64_t ldq, const uint8_t* S,
                              int64_t lds, void* Y, int64_t ldy, hipStream_t s);
-// Products: M > 64; M <= 64 (and its wave-private form); 16-bit A.
-hipError_t launch_product_tile(const Params& p, hipStream_t s);
+// Products with MX4 and with 16-bit A (k_mx4_rows.hip, which chooses), and
+// the forms chosen: tiles, and wave-private strips of rb blocks of 16 rows.
 hipError_t launch_product(const Params& p, hipStream_t s);
-hipError_t launch_skinny(const Params& p, hipStream_t s);
-hipError_t launch_skinny16(In t, const Params& p, hipStream_t s);
 hipError_t launch_product16(In t, const Params& p, hipStream_t s);
+hipError_t launch_product_tile(const Params& p, hipStream_t s);
+hipError_t launch_skinny(const Params& p, int rb, int cols, hipStream_t s);
+hipError_t launch_skinny16(In t, const Params& p, int rb, int cols, hipStream_t s);
 
 }  // namespace mx4
 }  // namespace dgt

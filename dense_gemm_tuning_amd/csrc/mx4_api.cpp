@@ -83,9 +83,7 @@ int product(bool mx, DType t, int M, int N, int K, float alpha, const void* A, i
     p.SB = SB; p.ldsb = ldsb;
     p.C = C; p.ldc = ldc;
     p.bias = bias;
-    if (!mx) return status_of(mx4::launch_product16(in_of(t), p, s));
-    return status_of(M > dgt::kSkinnyMaxM ? mx4::launch_product_tile(p, s)
-                                          : mx4::launch_product(p, s));
+    return status_of(mx ? mx4::launch_product(p, s) : mx4::launch_product16(in_of(t), p, s));
 }
 
 }  // namespace

@@ -167,11 +167,18 @@ def small_ints(rng, rows, K):
 WIDE = [(1, 14337, 33), (8, 16400, 160), (16, 28673, 97), (20, 9000, 544), (32, 16500, 300), (40, 17000, 1056),
         (64, 33000, 130), (100, 9000, 320)]
 
+# Few outputs and a long K on small workgroups (16 x 16, 16 x 32, 16 x 64 and
+# 32 x 32 outputs), one round of 64 x 64 ones, and tiles of 128 and 256 with
+# and without edges and K tails.
+MID = [(48, 1024, 2080), (256, 512, 1000), (256, 1024, 333), (64, 4096, 700), (128, 2048, 4100), (128, 4096, 5000),
+       (600, 64, 4500), (1030, 40, 9000), (600, 900, 1100), (1024, 768, 1024), (4096, 4096, 96), (3000, 3100, 544),
+       (4096, 4096, 512), (4000, 4100, 512)]
+
 
 # Bit-exact: MX4 operands are multiples of 1/4 of at most 24, so products are
 # multiples of 1/16 of at most 576 and every partial sum is below 576 K * 16 <
 # 2^24 units for K <= 1820; beyond that the operands' scales are 2^-1 .. 2^0.
-@pytest.mark.parametrize("M,N,K", SHAPES + WIDE)
+@pytest.mark.parametrize("M,N,K", SHAPES + WIDE + MID)
 @pytest.mark.parametrize("kind", ["mx4", "bf16", "f16"])
 def test_product_exact_values(M, N, K, kind):
     say("product", M, N, K, kind)
@@ -230,14 +237,14 @@ def test_product_real_values(M, N, K, kind):
     assert torch.equal(C, C2)  # run to run
 
 
-@pytest.mark.parametrize("M", [3, 20, 100])
+@pytest.mark.parametrize("M,N", [(3, 70), (20, 70), (100, 70), (40, 17000), (64, 6000), (600, 900)])
 @pytest.mark.parametrize("kind", ["mx4", "bf16", "f16"])
-def test_product_extreme_scales(M, kind):
+def test_product_extreme_scales(M, N, kind):
     """NaN blocks reach exactly the outputs they feed; scales near both ends of
     the range with factors that bring the product back into it; f16
     activations against weights far outside f16's range."""
-    N, K = 70, 160
-    rng = rng_for(M, 11)
+    K = 160
+    rng = rng_for(M, N, 11)
     B, SB, _ = int_operand(rng, N, K)
     SB[:, :5] = torch.from_numpy(rng.integers(1, 4, (N, 5), dtype=np.uint8)).cuda()  # 2^-126 ..
     SB[9, 2] = 255
@@ -282,13 +289,13 @@ def test_infinite_activations_and_zero_codes():
         np.testing.assert_array_equal(C.double().cpu().numpy(), want)
 
 
-@pytest.mark.parametrize("M", [5, 64, 200])
+@pytest.mark.parametrize("M,N", [(5, 150), (64, 150), (200, 150), (20, 9000), (64, 6000), (600, 900)])
 @pytest.mark.parametrize("kind", ["mx4", "bf16", "f16"])
-def test_product_strided_storage(M, kind):
+def test_product_strided_storage(M, N, kind):
     """Padded pitches everywhere, misaligned 16-bit rows, NaN and junk behind
     every row, a guard band around C."""
-    N, K = 150, 330
-    rng = rng_for(M, 5)
+    K = 330
+    rng = rng_for(M, N, 5)
     B, SB, b = int_operand(rng, N, K)
     Bf = torch.full((N, B.shape[1] + 48), 0x77, dtype=torch.uint8, device="cuda")
     Bf[:, :B.shape[1]] = B
