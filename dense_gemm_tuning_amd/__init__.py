@@ -501,6 +501,7 @@ def gemm_stream(A, B, C, alpha: float = 1.0, beta: float = 0.0, workspace=None, 
 # The calls below are made for decode steps of a few microseconds, so their
 # checks read every tensor attribute once and ask the library nothing.
 
+_INT_MAX = 2 ** 31 - 1  # the C entry points take sizes and pitches as int
 _FLOAT_CODES = None  # torch dtype -> enum gemm_dtype
 
 
@@ -527,7 +528,10 @@ def _matrix(t, name):
     if step != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name} must be row-major with unit column stride")
     if rows <= 1 or cols == 0:
-        pitch = max(pitch, cols, 1)
+        pitch = max(cols, 1)
+    if rows > _INT_MAX or cols > _INT_MAX or pitch > _INT_MAX:
+        raise ValueError(f"{name}: sizes and row pitch must be below 2^31, got {rows} x {cols}, "
+                         f"pitch {pitch}")
     return rows, cols, pitch
 
 
@@ -709,6 +713,7 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
         return (t[0], t.stride(0) if batch > 1 else 0) if t.dim() == 3 else (t, 0)
 
     (G2, sg), (O2, so) = mat(G), mat(O)
+    (_, _, ldg), (_, _, ldo) = _matrix(G2, "G"), _matrix(O2, "O")
     need = gemm_orthogonalize_workspace_size(M, N, batch)
     if need < 0:
         return need
@@ -721,6 +726,6 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
             with torch.cuda.stream(on):
                 workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
     a, b, c = (float(x) for x in coefficients)
-    return _call_on(index, stream, _load().gemm_orthogonalize, dtype, M, N, G2.data_ptr(), _ld(G2),
-                    sg, O2.data_ptr(), _ld(O2), so, batch, int(steps), a, b, c, float(eps),
+    return _call_on(index, stream, _load().gemm_orthogonalize, dtype, M, N, G2.data_ptr(), ldg,
+                    sg, O2.data_ptr(), ldo, so, batch, int(steps), a, b, c, float(eps),
                     workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -377,7 +377,8 @@ int gemm_mx4(int M, int N, int K, float alpha, const uint8_t* A, int lda,
 
 /* The same with 16-bit A (GEMM_DTYPE_BF16 or GEMM_DTYPE_F16, M x K, row pitch
  * lda elements, any alignment) against MX4 B: the products of a 16-bit and a
- * 4-bit value are exact and summed in fp32.  For batches of up to some
+ * 4-bit value are exact and summed in fp32 (with BF16 A a weight of 2^128 or
+ * more, which gemm_mx4_quantize never writes, counts as infinite).  For batches of up to some
  * hundred rows: from about 800 (BF16) or 300 (FP16) on, gemm_mx4_dequantize
  * and the dense product take less time, where there is room for the result. */
 int gemm_mx4_a16(int dtype, int M, int N, int K, float alpha, const uint16_t* A,

@@ -450,3 +450,55 @@ def test_training_products_of_a_linear_layer():
     scale = (np.abs(g) * ((np.abs(X.double().cpu().numpy()) + np.abs(X1.double().cpu().numpy()))
                           @ np.abs(w).T)).sum()
     assert abs(diff - (dX * moved).sum()) <= (I + 4) * 2.0 ** -23 * scale
+
+
+@pytest.mark.parametrize("M,N", [(64, 6000), (600, 900), (2, 300)])
+def test_products_captured_at_each_form(M, N):
+    """Shared strips, tiles and wave-private strips captured together and
+    replayed on new operands, with eager work between the replays."""
+    K = 640
+    rng = rng_for(M, N, 41)
+    B, SB, b = int_operand(rng, N, K)
+    A, SA, _ = int_operand(rng, M, K)
+    X = torch.empty(M, K, dtype=torch.float16, device="cuda")
+    C, D = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+
+    def step():
+        dgt.check(dgt.gemm_quantized(A, SA, B, SB, C))
+        dgt.check(dgt.gemm_quantized(X, None, B, SB, D))
+
+    X.zero_()
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        A2, SA2, a = int_operand(rng, M, K)
+        A.copy_(A2), SA.copy_(SA2)
+        x = small_ints(rng, M, K)
+        X.copy_(torch.from_numpy(x))
+        C.fill_(float("nan")), D.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(C.double().cpu().numpy(), a @ b.T)
+        assert np.array_equal(D.double().cpu().numpy(), x @ b.T)
+
+
+def test_one_operand_on_both_sides_and_tall_products():
+    """A x A^T with one operand given twice; far more rows than tiles of columns."""
+    rng = rng_for(42)
+    A, SA, a = int_operand(rng, 333, 320)
+    C = torch.empty(333, 333, device="cuda")
+    dgt.check(dgt.gemm_quantized(A, SA, A, SA, C))
+    assert np.array_equal(C.double().cpu().numpy(), a @ a.T)
+    M, N, K = 70001, 1, 64
+    B, SB, b = int_operand(rng, N, K)
+    T, ST, t = int_operand(rng, M, K)
+    C = torch.empty(M, N, device="cuda")
+    dgt.check(dgt.gemm_quantized(T, ST, B, SB, C))
+    assert np.array_equal(C.double().cpu().numpy(), t @ b.T)
+    x = small_ints(rng, M, K)
+    for dt in (torch.bfloat16, torch.float16):
+        dgt.check(dgt.gemm_quantized(torch.from_numpy(x).to(dt).cuda(), None, B, SB, C))
+        assert np.array_equal(C.double().cpu().numpy(), x @ b.T)

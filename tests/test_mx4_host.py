@@ -156,6 +156,19 @@ def test_torch_calls_refuse_host_tensors_and_wrong_shapes():
         dgt.orthogonalize(X, O, workspace=_u8(8, 8).t())
 
 
+def test_torch_calls_refuse_pitches_past_an_int():
+    """A pitch that the C entry points' int would cut is refused; a single
+    row's, which is never used, is not looked at."""
+    far = torch.empty_strided((2, 64), (2 ** 32 + 64, 1), dtype=torch.bfloat16, device="meta")
+    q, s = _u8(2, 32), _u8(2, 16)
+    c = torch.empty(2, 2)
+    for call in (lambda: dgt.quantize_mx4(far, q, s), lambda: dgt.dequantize_mx4(q, s, far),
+                 lambda: dgt.gemm_quantized(far, None, q, s, c)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert dgt._matrix(far[:1], "X") == (1, 64, 64)
+
+
 def test_plain_format_pins():
     """The plain model itself: every code stands for its value and quantises
     back to itself; ties go to the even code; saturation; zero and NaN blocks."""

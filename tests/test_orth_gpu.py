@@ -285,3 +285,49 @@ def test_large_in_place_and_replayed(M, N):
         assert torch.equal(got, O)
     dgt.check(dgt.orthogonalize(torch.zeros_like(G), O, workspace=ws))
     assert not O.any()
+
+
+def test_many_tiny_matrices():
+    """A batch large enough for the large tiles, of matrices far smaller than one."""
+    rng = np.random.default_rng(11)
+    G = torch.stack([matrix(rng, 24, 40, "f32") for _ in range(400)])
+    O = torch.full((400, 24, 40), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dgt.check(dgt.orthogonalize(G.cuda(), O))
+    got = O.double().cpu().numpy()
+    for z in range(400):
+        want = mp.newton_schulz(G[z].double().numpy(), 5, *COEF, 1e-7)
+        assert np.linalg.norm(got[z] - want) <= NORMWISE * np.linalg.norm(want), z
+
+
+@pytest.mark.parametrize("M,N", [(1, 70001), (70001, 2)])
+def test_very_long_matrices(M, N):
+    G = matrix(np.random.default_rng([M, N, 12]), M, N, "f32", "normal")
+    O = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dgt.check(dgt.orthogonalize(G.cuda(), O))
+    want = mp.newton_schulz(G.double().numpy(), 5, *COEF, 1e-7)
+    assert np.linalg.norm(O.double().cpu().numpy() - want) <= NORMWISE * np.linalg.norm(want)
+
+
+def test_two_graphs_with_a_workspace_each():
+    """Two captured calls replayed on two streams at once."""
+    rng = np.random.default_rng(13)
+    sets = []
+    for M, N in ((256, 256), (260, 2100)):
+        G = matrix(rng, M, N, "bf16").cuda()
+        want, O = torch.empty_like(G), torch.empty_like(G)
+        dgt.check(dgt.orthogonalize(G, want))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):  # the workspace comes from the graph's own pool
+            dgt.check(dgt.orthogonalize(G, O))
+        sets.append((graph, G, want, O, torch.cuda.Stream()))
+    for _ in range(3):
+        for _, _, _, O, _ in sets:
+            O.zero_()
+        torch.cuda.synchronize()
+        for graph, _, _, _, stream in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, want, O, _ in sets:
+            assert torch.equal(O, want)
