@@ -94,8 +94,8 @@ inline Plan make_plan(int M, int N, int batch) {
     p.s_size = (int64_t)p.n * p.lds;
     // Few tiles and a long k leave compute units idle: enough parts to give
     // each one a tile (two side by side where one does not go round), no part below 512 deep.
-    // 8192 x 1024 (36 tiles): 350 us for the whole call in 7 parts, 369 in
-    // 14; 2048 x 8192 (136 tiles): 887 in one, 771 in 3.
+    // 8192 x 1024 (36 tiles): 337 us for the whole call in 7 parts, 361 in 8,
+    // 345 in 14; 2048 x 8192 (136 tiles): 887 in one, 757 in 3.
     p.splits = 1;
     p.kc = p.k;
     const int64_t tiles = lower_tiles(p.n, kGramTile) * batch;
