@@ -502,15 +502,24 @@ def gemm_stream(A, B, C, alpha: float = 1.0, beta: float = 0.0, workspace=None, 
 # checks read every tensor attribute once and ask the library nothing.
 
 _INT_MAX = 2 ** 31 - 1  # the C entry points take sizes and pitches as int
-_FLOAT_CODES = None  # torch dtype -> enum gemm_dtype
+_torch = None  # the module, from the first torch-facing call below on
+_FLOAT_CODES = {}  # torch dtype -> enum gemm_dtype
+
+
+def _use_torch():
+    """torch, without an import statement's cost in every call."""
+    global _torch
+    if _torch is None:
+        import torch
+        _FLOAT_CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
+                             torch.float16: DTYPE_F16})
+        _torch = torch
+    return _torch
 
 
 def _float_code(t, name):
-    global _FLOAT_CODES
-    if _FLOAT_CODES is None:
-        import torch
-        _FLOAT_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
-                        torch.float16: DTYPE_F16}
+    if _torch is None:
+        _use_torch()
     code = _FLOAT_CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
@@ -537,8 +546,7 @@ def _matrix(t, name):
 
 def _bytes(t, name, rows):
     """(columns, pitch) of MX4 codes or scales of ``rows`` rows."""
-    import torch
-    if t.dtype is not torch.uint8:
+    if t.dtype is not (_torch or _use_torch()).uint8:
         raise TypeError(f"{name} must be uint8, got {t.dtype}")
     have, cols, pitch = _matrix(t, name)
     if have != rows:
@@ -558,7 +566,9 @@ def _fits(K, cols_q, cols_s, name):
 def _on_device(index, named):
     """Every non-empty (name, tensor) on GPU ``index`` (-1: the host)."""
     for name, t in named:
-        if (index < 0 or t.get_device() != index) and t.numel() > 0:
+        if t.get_device() == index >= 0:
+            continue
+        if t.numel() > 0:
             at = "" if index < 0 else f" on cuda:{index}"
             raise ValueError(f"{name} must be a GPU tensor{at}, got {t.device}")
 
@@ -567,7 +577,7 @@ def _call_on(index, stream, fn, *args):
     """fn(*args, stream handle) with GPU ``index`` current and, by default, the
     stream current there (the tensors may live on another GPU than the one the
     caller has current)."""
-    import torch
+    torch = _torch or _use_torch()
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     else:
@@ -633,7 +643,7 @@ def gemm_quantized(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=
     float32 [M, N], row-major; bias None or float32 [N].  With MX4 A the
     summation runs over every stored element: codes past a ragged K are zeros
     (quantize_mx4 writes them so).  Returns the status code."""
-    import torch
+    torch = _torch or _use_torch()
     if C.dtype is not torch.float32:
         raise TypeError("C must be float32")
     M, N, ldc = _matrix(C, "C")
@@ -690,7 +700,7 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     of at least gemm_orthogonalize_workspace_size bytes that no other call uses
     at the same time; when None one is allocated here with torch, for the
     stream the work runs on.  Returns the status code."""
-    import torch
+    torch = _torch or _use_torch()
     dtype = _float_code(G, "G")
     if O.dtype is not torch.bfloat16:
         raise TypeError("O must be bfloat16")
