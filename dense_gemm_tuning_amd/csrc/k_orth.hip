@@ -13,13 +13,14 @@
 //
 // Rounding.  The products' operands are FP16.  Each step multiplies what
 // rounding X adds in the weak singular directions by up to a (3.4 with the
-// usual coefficients, 484 over five steps), so rounding X itself to 16 bits
-// costs a result normwise 2 to 4e-3 against 1.7e-3 that its own bf16 rounding costs.
-// X is therefore kept as two halves hi + lo (22 bits) while more than two
-// steps are left; the products read hi, the term a X both.  What hi's rounding
-// E adds through the products reaches the weak directions only as (b S + c S S) E, small
-// where S is, and the result is 1.7 to 2.4e-3 off (matrices of 256 to
-// 1536, normal, low-rank, 1/i and 1/i^2 spectra; one half throughout: 2.2e-3 to 2e-2).
+// usual coefficients, 484 over five steps), so X rounded to 16 bits costs a matrix
+// of rank one 0.15, and 3.3e-3 if only the last two steps' X is, against 1.7e-3 that the
+// result's own bf16 rounding costs.  X is therefore kept as two halves hi + lo
+// (22 bits) in every step; the products read hi, the term a X both.  What hi's
+// rounding E adds through the products reaches the weak directions only as (b S + c S S) E,
+// small where S is.  The result is normwise 1.7e-3 off for exact low rank and 1/i^2
+// spectra, 1.7 to 1.9e-3 for 1/i, 1.7 to 2.5e-3 for normal values or a floor of them, where the
+// roundings of S and B count too (matrices of 200 to 4096, five steps).
 //
 // FP16's range: |X| <= |X|_2, about 1, but its elements are near
 // 1/sqrt(max(M, N)) and the Gram matrix's smaller still, so X is held times
@@ -270,8 +271,7 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void symmetric_kernel(
         });
 }
 
-// X' = a (hi + lo) + f * sums: two halves, or (kLast) the result in bf16.  lo
-// or lo2 is null where X or X' is kept in one half.
+// X' = a (hi + lo) + f * sums: two halves, or (kLast) the result in bf16.
 struct Update {
     const _Float16 *hi, *lo;
     _Float16 *hi2, *lo2;
@@ -304,8 +304,7 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams
                     const int64_t at = xz + (int64_t)row * u.ldx + col;
                     if (!kEdge || (row < p.M && col < p.N)) {
                         h[ti & 1][i] = *reinterpret_cast<const halfx8*>(u.hi + at);
-                        if (u.lo) l[ti & 1][i] = *reinterpret_cast<const halfx8*>(u.lo + at);
-                        else l[ti & 1][i] = halfx8{};
+                        l[ti & 1][i] = *reinterpret_cast<const halfx8*>(u.lo + at);
                     }
                 }
             };
@@ -343,7 +342,7 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams
                         halfx8 nh, nl;
                         split8(x, nh, nl);
                         *reinterpret_cast<halfx8*>(u.hi2 + at) = nh;
-                        if (u.lo2) *reinterpret_cast<halfx8*>(u.lo2 + at) = nl;
+                        *reinterpret_cast<halfx8*>(u.lo2 + at) = nl;
                     }
                 }
             }
@@ -422,12 +421,6 @@ __global__ __launch_bounds__(NT) void gram_join_kernel(const float* partial, int
     if (col0 + col < n && row0 + half < n)
         *reinterpret_cast<halfx8*>(S + (col0 + col) * ld + row0 + half) = t;
 }
-
-// Whether X before step i is kept in two halves: what rounding it to one adds in the
-// weak directions grows by a factor up to a in each step left, so the last
-// two steps' X are not (12 times half an FP16 step), which saves a third of the
-// update's traffic there.
-bool two_halves(int i, int steps) { return i == 0 || steps - i > 2; }
 
 unsigned grid_for(int64_t items) {
     const int64_t g = (items + NT - 1) / NT;
@@ -573,8 +566,8 @@ hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
                                          c.c * (kPolyScale / (kGramScale * kGramScale)),
                                          c.b * (kPolyScale / kGramScale), s);
         if (e != hipSuccess) return e;
-        u.hi = hi[r]; u.lo = two_halves(i, c.steps) ? lo[r] : nullptr;
-        u.hi2 = hi[w]; u.lo2 = two_halves(i + 1, c.steps) ? lo[w] : nullptr;
+        u.hi = hi[r]; u.lo = lo[r];
+        u.hi2 = hi[w]; u.lo2 = lo[w];
         const bool last = i + 1 == c.steps;
         if (tall) {
             g = operands(p, p.M, p.N, p.n, hi[r], p.ldx, p.x_size, B, p.lds, p.s_size);
