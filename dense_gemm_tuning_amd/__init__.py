@@ -696,10 +696,11 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     X <- a*X + (b*S + c*S*S)*X from X = G / (|G| + eps) (gemm_orthogonalize;
     the default coefficients are the quintic's that Muon uses).  G is float32,
     bfloat16 or float16 and O bfloat16, both [M, N] or [batch, M, N] with
-    row-major matrices; O may be G.  ``workspace`` is a contiguous GPU tensor
-    of at least gemm_orthogonalize_workspace_size bytes that no other call uses
-    at the same time; when None one is allocated here with torch, for the
-    stream the work runs on.  Returns the status code."""
+    row-major matrices, M at most 2^26 and N at most 2^24; O may be G.
+    ``workspace`` is a contiguous GPU tensor of at least
+    gemm_orthogonalize_workspace_size bytes that no other call uses at the same
+    time; when None one is allocated here with torch, for the stream the work
+    runs on.  Returns the status code."""
     torch = _torch or _use_torch()
     dtype = _float_code(G, "G")
     if O.dtype is not torch.bfloat16:

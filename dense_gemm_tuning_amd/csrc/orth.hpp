@@ -9,6 +9,13 @@
 namespace dgt {
 namespace orth {
 
+// Sizes.  A workgroup of the tile kernels copies up to 64 rows of X through one
+// descriptor with 32-bit byte offsets (mfma16_tile.hpp), so a padded row is at
+// most kMaxBufferPitch elements.  X is held times 2^scale_exp of the larger
+// dimension, 2^13 up to 2^26: its elements, below 4 as its singular values are,
+// stay below FP16's 65504 (2^14 would not).
+constexpr int kMaxCols = (int)kMaxBufferPitch, kMaxRows = 1 << 26;
+
 // Partial sums of squares of a matrix: a workgroup's 256 lanes take a few runs
 // of 8 elements each.
 constexpr int kMaxNormParts = 1024;

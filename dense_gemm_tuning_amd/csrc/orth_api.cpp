@@ -18,9 +18,11 @@ namespace orth = dgt::orth;
 constexpr int kMaxSteps = 64;
 constexpr int kMaxBatch = 65535;  // one grid dimension
 
-// Matrices whose padded size cannot be a workspace offset.
+// Rows past the tiles' 32-bit copy offsets, columns past FP16's range
+// (orth.hpp), or matrices whose padded size cannot be a workspace offset.
 bool too_large(int M, int N, int batch) {
-    return (double)M * ((double)N + 64) * batch > (double)(int64_t(1) << 46);
+    return M > orth::kMaxRows || N > orth::kMaxCols ||
+           (double)M * ((double)N + 64) * batch > (double)(int64_t(1) << 46);
 }
 
 }  // namespace

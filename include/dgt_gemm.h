@@ -413,15 +413,17 @@ int gemm_mx4_a16(int dtype, int M, int N, int K, float alpha, const uint16_t* A,
  * stay untouched until the work on `stream` has finished; calls that may run
  * at the same time (other streams, captured graphs) need workspaces of their
  * own.  G is read completely before O is written, so O may be G's memory.
- * The problems' O ranges must be disjoint. steps must be
- * 1 to 64, a, b, c finite and eps >= 0; batch 1 to 65535 (0 does nothing). */
+ * The problems' O ranges must be disjoint.  steps must be 1 to 64, a, b, c
+ * finite and eps >= 0; batch 1 to 65535 (0 does nothing).  M is at most 2^26
+ * and N at most 2^24 (GEMM_ERR_DIM otherwise, in both calls): longer rows pass the
+ * kernels' 32-bit offsets, more rows leave FP16's range. */
 int gemm_orthogonalize(int dtype, int M, int N, const void* G, int ldg,
                        int64_t stride_g, uint16_t* O, int ldo, int64_t stride_o,
                        int batch, int steps, float a, float b, float c, float eps,
                        void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace gemm_orthogonalize needs (0 for an empty call), or a
- * negative status for negative arguments.  Host only. */
+ * negative status for arguments outside its limits.  Host only. */
 int64_t gemm_orthogonalize_workspace_size(int M, int N, int batch);
 
 /* The rung GEMM_VARIANT_AUTO picks for this call (dtype: enum gemm_dtype;
