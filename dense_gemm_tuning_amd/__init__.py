@@ -557,10 +557,17 @@ def _bytes(t, name, rows):
 
 
 def _fits(K, cols_q, cols_s, name):
+    """Rows of ``cols_q`` code and ``cols_s`` scale bytes hold K elements.  Wider
+    ones are padded storage, unless both widths are what mx4_empty makes for
+    more elements: then the operand is one of another K (its blocks past K would go
+    unread, or unwritten)."""
     need_q, need_s = (K + 31) // 32 * 16, (K + 511) // 512 * 16  # gemm_mx4_*_pitch
     if cols_q < need_q or cols_s < need_s:
         raise ValueError(f"{name}: {K} elements need rows of {need_q} code and {need_s} scale "
                          f"bytes, got {cols_q} and {cols_s}")
+    if cols_q != need_q and cols_q % 16 == 0 and cols_s == (cols_q + 255) // 256 * 16:
+        raise ValueError(f"{name}: an operand of {2 * cols_q - 31} to {2 * cols_q} elements a row, "
+                         f"not of {K} (of padded storage pass [:, :{need_q}] of the codes)")
 
 
 def _on_device(index, named):
@@ -602,9 +609,9 @@ def mx4_empty(rows: int, K: int, device="cuda"):
 def quantize_mx4(X, Q, S, trans: bool = False, stream=None) -> int:
     """(Q, S) <- op(X) in MX4 blocks along its columns (gemm_mx4_quantize);
     op(X) is X, or X transposed when ``trans``.  X is float32, bfloat16 or
-    float16, row-major; Q and S as ``mx4_empty`` makes them for op(X).  Blocks
-    run along the summation index of the product the operand is for.  Returns
-    the status code."""
+    float16, row-major; Q and S as ``mx4_empty`` makes them for op(X), or views
+    of wider storage.  Blocks run along the summation index of the product the
+    operand is for.  Returns the status code."""
     dtype = _float_code(X, "X")
     rows, cols, ldx = _matrix(X, "X")
     M, K = (cols, rows) if trans else (rows, cols)
@@ -640,7 +647,8 @@ def gemm_quantized(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=
     """C <- alpha*A*B^T + beta*C + bias with B an MX4 operand of N rows (codes
     B, scales SB) and A either one of M rows (codes A, scales SA: gemm_mx4) or
     a bfloat16 / float16 [M, K] tensor with SA None (gemm_mx4_a16).  C is
-    float32 [M, N], row-major; bias None or float32 [N].  With MX4 A the
+    float32 [M, N], row-major; bias None or float32 [N].  With 16-bit A, K is
+    A's, and B and SB of the widths of another K are refused.  With MX4 A the
     summation runs over every stored element: codes past a ragged K are zeros
     (quantize_mx4 writes them so).  Returns the status code."""
     torch = _torch or _use_torch()
