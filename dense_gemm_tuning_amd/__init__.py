@@ -740,8 +740,12 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
         else:  # in that stream's order, so that a later call cannot get it too early
-            on = (stream if hasattr(stream, "cuda_stream")
-                  else torch.cuda.ExternalStream(stream, device=O.device))
+            if hasattr(stream, "cuda_stream"):
+                on = stream
+            elif stream == 0:  # ExternalStream takes 0 for "any stream of the pool"
+                on = torch.cuda.default_stream(O.device)
+            else:
+                on = torch.cuda.ExternalStream(stream, device=O.device)
             with torch.cuda.stream(on):
                 workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
     a, b, c = (float(x) for x in coefficients)
