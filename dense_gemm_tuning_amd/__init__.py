@@ -602,6 +602,8 @@ def mx4_empty(rows: int, K: int, device="cuda"):
     """Uninitialised storage of a rows x K MX4 operand: (codes, scales), two
     uint8 tensors of the smallest row pitches."""
     import torch
+    if K > _INT_MAX:
+        raise ValueError(f"K must be below 2^31, got {K}")
     return (torch.empty(rows, gemm_mx4_code_pitch(K), dtype=torch.uint8, device=device),
             torch.empty(rows, gemm_mx4_scale_pitch(K), dtype=torch.uint8, device=device))
 
@@ -721,12 +723,14 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         named.append(("workspace", workspace))
+    batch = G.shape[0] if G.dim() == 3 else 1
+    if batch > _INT_MAX or abs(int(steps)) > _INT_MAX:
+        raise ValueError(f"batch and steps must be below 2^31, got {batch} and {steps}")
     index = O.get_device()
     _on_device(index, named)
     if G.numel() == 0:
         return GEMM_OK
     M, N = G.shape[-2:]
-    batch = G.shape[0] if G.dim() == 3 else 1
 
     def mat(t):
         return (t[0], t.stride(0) if batch > 1 else 0) if t.dim() == 3 else (t, 0)

@@ -4,6 +4,7 @@ offsets and FP16 ranges do not hold.  Nothing here reaches a launch."""
 import os
 
 import pytest
+import torch
 
 import dense_gemm_tuning_amd as dgt
 
@@ -38,3 +39,16 @@ def test_sizes_at_the_limits_are_taken(M, N):
     need = dgt.gemm_orthogonalize_workspace_size(M, N, 1)
     assert need >= 8 * M * N  # X in two halves, twice
     assert call(M, N) == call(M, N, nbytes=need - 1) == dgt.GEMM_ERR_WORKSPACE
+
+
+def test_counts_past_an_int_are_refused():
+    """The C entry points take them as int, which would cut them: a batch of
+    2^32 + 1 to 1, as many steps plus four to five."""
+    far = torch.empty(2 ** 32 + 1, 1, 1, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        dgt.orthogonalize(far, far)
+    one = torch.zeros(1, 1, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        dgt.orthogonalize(one, one, steps=2 ** 32 + 5)
+    with pytest.raises(ValueError, match="2\\^31"):
+        dgt.mx4_empty(2, 2 ** 32 + 64, device="meta")
