@@ -274,10 +274,10 @@ hipError_t quantize(bool trans, int M, int K, const void* X, int64_t ldx, uint8_
     constexpr int esz = T == In::F32 ? 4 : 2;
     const int nb = blocks(K), runs_per_row = (int)(scale_pitch(K) / kScaleRow);
     if (trans) {
-        const int tiles_m = (M + TCOLS - 1) / TCOLS;
+        const int tiles_m = (int)(((int64_t)M + TCOLS - 1) / TCOLS);
         const int slots = runs_per_row * kScaleRow;
         const int64_t wgs = (int64_t)tiles_m * (slots / TBLK);
-        if (wgs > 0x7fffffff) return hipErrorInvalidConfiguration;
+        if (!launchable(wgs, TNT)) return hipErrorInvalidConfiguration;
         const bool pairs = reinterpret_cast<uintptr_t>(X) % (2 * esz) == 0 && ldx % 2 == 0;
         hipLaunchKernelGGL(quantize_columns_kernel<T>, dim3((unsigned)wgs), dim3(TNT), 0, s, X,
                            ldx, M, K, nb, slots, tiles_m, Q, ldq, S, lds, pairs);

@@ -334,10 +334,10 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void mx4_rows_kernel(Params p, int c
 
 template <Kind KA, int RBT, int COLS, int KS, int ROWB, int NS>
 hipError_t launch_strips(const Params& p, int cols, hipStream_t s) {
-    const int mchunks = (p.M + 16 * RBT - 1) / (16 * RBT);
+    const int mchunks = (int)(((int64_t)p.M + 16 * RBT - 1) / (16 * RBT));
     const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
     const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
-    if (wgs > 0x7fffffff || 8 * (int64_t)mchunks > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(wgs, NWAVE * 64)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((mx4_rows_kernel<KA, RBT, COLS, KS, ROWB, NS>), dim3((unsigned)wgs),
                        dim3(NWAVE * 64), 0, s, p, cols, blocks(p.K), mchunks);
     return hipGetLastError();
@@ -349,7 +349,7 @@ hipError_t launch_strips(const Params& p, int cols, hipStream_t s) {
 template <Kind KA, int RBT, int NS64, int NS128>
 hipError_t launch_width(const Params& p, hipStream_t s) {
     constexpr int KS = 4, ROWB = KA == Kind::MX4 ? 256 : 128;
-    const int64_t chunks = (p.M + 16 * RBT - 1) / (16 * RBT);
+    const int64_t chunks = ((int64_t)p.M + 16 * RBT - 1) / (16 * RBT);
     auto strips = [&](int c) { return ((int64_t)p.N + c - 1) / c * chunks; };
     // (FP16 at 64 rows: 128 columns do not fit the registers)
     if (strips(64) <= dma::kCUs || (KA == Kind::F16 && RBT == 4))

@@ -405,10 +405,10 @@ __global__ __launch_bounds__(NW * 64, 1) void mx4_skinny_kernel(Params p, int co
 template <Kind KA, int RB, int ROWB, int NS, int NG, int GR>
 hipError_t launch_cfg(const Params& p, hipStream_t s) {
     constexpr int cols = NG * GR;
-    const int mchunks = (p.M + 16 * RB - 1) / (16 * RB);
+    const int mchunks = (int)(((int64_t)p.M + 16 * RB - 1) / (16 * RB));
     const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
     const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
-    if (wgs > 0x7fffffff || 8 * (int64_t)mchunks > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (!launchable(wgs, NW * 64)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((mx4_skinny_kernel<KA, RB, ROWB, NS, NG, GR>), dim3((unsigned)wgs),
                        dim3(NW * 64), 0, s, p, cols, blocks(p.K), mchunks);
     return hipGetLastError();

@@ -351,11 +351,12 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void mx4_tile_kernel(Params p
 
 template <int R>
 hipError_t launch_tiles(const Params& p, hipStream_t s) {
-    const int tiles_m = (p.M + R - 1) / R, tiles_n = (p.N + R - 1) / R, nb = blocks(p.K);
-    const int64_t wgs = (int64_t)tiles_m * tiles_n;
-    if (wgs > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const int64_t tiles_m = ((int64_t)p.M + R - 1) / R, tiles_n = ((int64_t)p.N + R - 1) / R;
+    const int64_t wgs = tiles_m * tiles_n;
+    const int nb = blocks(p.K);
+    if (!launchable(wgs, NT)) return hipErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, s, p, tiles_n, nb);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, s, p, (int)tiles_n, nb);
         return hipGetLastError();
     };
     if (nb % 16 != 0) return go(mx4_tile_kernel<R, true, true>);
@@ -367,8 +368,9 @@ hipError_t launch_tiles(const Params& p, hipStream_t s) {
 
 // Tile size as for the 16-bit kernel.
 hipError_t launch_product_tile(const Params& p, hipStream_t s) {
-    const int64_t t256 = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256);
-    const int64_t t128 = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
+    const int64_t M = p.M, N = p.N;
+    const int64_t t256 = (M + 255) / 256 * ((N + 255) / 256);
+    const int64_t t128 = (M + 127) / 128 * ((N + 127) / 128);
     const double time256 = (double)((t256 + kCUs - 1) / kCUs) * 4.0;
     const double time128 = (double)((t128 + 2 * kCUs - 1) / (2 * kCUs)) * 2.0 * 1.22;
     return time128 < time256 ? launch_tiles<128>(p, s) : launch_tiles<256>(p, s);

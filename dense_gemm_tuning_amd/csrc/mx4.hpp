@@ -28,6 +28,11 @@ inline int64_t scale_pitch(int K) {
     return (int64_t)kScaleRow * ((blocks(K) + kScaleRow - 1) / kScaleRow);
 }
 
+// Whether one launch holds that many workgroups (fewer than 2^32 threads).
+inline bool launchable(int64_t workgroups, int threads) {
+    return workgroups < (int64_t(1) << 32) / threads;
+}
+
 struct Params {
     int M, N, K;
     float alpha, beta;

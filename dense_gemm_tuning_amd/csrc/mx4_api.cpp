@@ -37,7 +37,11 @@ Range rows_range(const void* base, int rows, int64_t row_bytes, int64_t pitch_by
                        1);
 }
 
-int status_of(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
+int status_of(hipError_t e) {
+    return e == hipSuccess                      ? GEMM_OK
+           : e == hipErrorInvalidConfiguration ? GEMM_ERR_DIM  // more workgroups than a launch holds
+                                               : GEMM_ERR_LAUNCH;
+}
 
 // The checks and the launch shared by the two products; t is the format of A
 // (MX4 when mx is set).

@@ -75,7 +75,8 @@ enum gemm_dtype { GEMM_DTYPE_F32 = 0, GEMM_DTYPE_BF16 = 1, GEMM_DTYPE_F16 = 2 };
 
 enum gemm_status {
     GEMM_OK = 0,
-    GEMM_ERR_DIM = -1,          /* M, N or K negative                        */
+    GEMM_ERR_DIM = -1,          /* M, N or K negative; MX4 and
+                                   orthogonalisation: past their limits      */
     GEMM_ERR_LD = -2,           /* lda < max(1,K), ldb < max(1,N) or
                                    ldc < max(1,N)                            */
     GEMM_ERR_NULL = -3,         /* NULL A/B (when read) or C with a
@@ -339,7 +340,10 @@ int64_t gemm_streamk_workspace_size(int dtype, int M, int N, int K);
  * X^T along the batch.
  *
  * Checks run in this order: dtype and flags, dimensions, pitches, quick
- * return for an empty result, null pointers, alignment, overlap. */
+ * return for an empty result, null pointers, alignment, overlap.  A call that
+ * needs more workgroups than one launch holds (2^32 threads: products from
+ * 2^23 strips of 64 rows by 128 columns on, 16-bit A off 16-byte rows from strips of
+ * 16 rows) is GEMM_ERR_DIM. */
 
 #define DGT_GEMM_MX4_MAX_PITCH (1 << 24)
 

@@ -39,3 +39,20 @@ def test_views_of_padded_storage_and_equal_block_counts_pass():
     for b, s in ((wide[:, :176], scales[:, :16]), (wide, scales), (wide[:, :176], scales), (B, SB)):
         with pytest.raises(ValueError, match="GPU tensor"):
             dgt.gemm_quantized(A, None, b, s, C)
+
+
+def test_more_workgroups_than_a_launch_holds_are_refused():
+    """2^32 threads are one launch's limit; the counts are not cut on the way."""
+    A, SA, B, SB, C = (i << 50 for i in range(1, 6))
+    top = 2 ** 31 - 1
+
+    def mx4(M, N, K=32):
+        return dgt.gemm_mx4(M, N, K, 1.0, A, 16, SA, 16, B, 16, SB, 16, 0.0, C, N)
+
+    def a16(M, N, dtype=dgt.DTYPE_BF16, lda=32):
+        return dgt.gemm_mx4_a16(dtype, M, N, 32, 1.0, A, lda, B, 16, SB, 16, 0.0, C, N)
+
+    assert mx4(top, 1) == mx4(1, top) == mx4(2 ** 22, 2 ** 22) == dgt.GEMM_ERR_DIM
+    assert a16(top, 1) == a16(1, top) == a16(2 ** 26, 64) == dgt.GEMM_ERR_DIM
+    assert a16(top, 1, dgt.DTYPE_F16, 33) == a16(top, 1, dgt.DTYPE_F16) == dgt.GEMM_ERR_DIM
+    assert dgt.gemm_mx4_quantize(dgt.DTYPE_BF16, 1, top, 32, A, top, B, 16, SB, 16) == dgt.GEMM_ERR_DIM
