@@ -366,7 +366,12 @@ hipError_t launch_tiles(const Params& p, hipStream_t s) {
 
 }  // namespace
 
-// Tile size as for the 16-bit kernel.
+// Tile size by the wave model of the 16-bit kernel.  On MX4 operands, us (128 /
+// 256, the choice last): 1024^3 8.3 / 11.0 128, 2048^3 11.9 / 16.4 128, 3000^3 36.3 / 32.6 256,
+// 4096^3 47.4 / 43.8 256, 6144^3 143.8 / 139.7 256, 8192^3 324 / 261 256, 1024 x 28672 x 8192
+// 165 / 123 256.  With a short K the 256-tile's longer prologue and epilogue outweigh its
+// loop and the model, which does not look at K, is wrong by up to a quarter: 4096 x 4096 x 512
+// 15.7 / 20.5 256, 8192 x 8192 x 1024 63.3 / 77.4 256, 3000 x 3100 x 544 20.9 / 22.7 256.
 hipError_t launch_product_tile(const Params& p, hipStream_t s) {
     const int64_t M = p.M, N = p.N;
     const int64_t t256 = (M + 255) / 256 * ((N + 255) / 256);

@@ -361,7 +361,7 @@ __device__ __forceinline__ void lower_pair(int idx, int& bm, int& bn) {
 // floats to its place in `partial`.  XCD x takes a contiguous range of the
 // (tiles * splits * batch) workgroups, tiles fastest: it reads one or two parts
 // of X, each many times, where workgroups in launch order read all of X through every
-// L2 (a whole call on 8192 x 1024 337 us against 349, on 1024 x 8192 331 against 351).
+// L2 (a whole call on 8192 x 1024 329 us against 348, on 1024 x 8192 328 against 353).
 template <bool TA, bool TB, bool kTail>
 __global__ __launch_bounds__(NT, 2) void gram_part_kernel(GemmParams p, int kc, int splits,
                                                           int tiles, float* partial) {
@@ -439,7 +439,9 @@ GemmParams operands(const Plan& p, int M, int N, int K, const _Float16* A, int64
 }
 
 // The tile size with less time by the wave model of the 16-bit kernel (t256,
-// t128: tiles of the launch).
+// t128: tiles of the launch).  Whole calls, us (all 128 / all 256 / as chosen): 1024^2 218 /
+// 373 / 219, 2600^2 617 / 862 / 613, 2048 x 8192 816 / 902 / 797, 4096^2 1832 / 1563 / 1561,
+// 16 x 1024^2 666 / 640 / 640, 16 x 2048^2 3903 / 3497 / 3494.
 bool use128(int64_t t256, int64_t t128) {
     const double time256 = (double)((t256 + kCUs - 1) / kCUs) * 4.0;
     const double time128 = (double)((t128 + 2 * kCUs - 1) / (2 * kCUs)) * 2.0 * 1.22;

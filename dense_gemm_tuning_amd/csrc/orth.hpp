@@ -49,8 +49,9 @@ struct SmallPlan {
 
 // Whether a call takes them: products whose 32 x 32 tiles, a workgroup each,
 // make three rounds of the compute units at most.  Measured, us (these / the tile
-// kernels): 64^2 45 / 81, 256^2 59 / 128, 512^2 84 / 164, 768^2 192 / 207, 1024^2 286 / 233,
-// 256 x 1024 76 / 148, 256 x 4096 165 / 164, 4 x 256^2 68 / 131, 16 x 256^2 136 / 127.
+// kernels): 64^2 51 / 80, 256^2 60 / 109, 512^2 85 / 146, 768^2 194 / 188, 900^2 281 / 234,
+// 1024^2 290 / 216, 256 x 1024 78 / 130, 640 x 1280 187 / 184, 256 x 4096 167 / 138,
+// 4 x 256^2 69 / 112, 16 x 256^2 135 / 109.
 inline bool is_small(int M, int N, int batch) {
     const int64_t n = ((M < N ? M : N) + 63ll) / 64 * 64, k = ((M < N ? N : M) + 63ll) / 64 * 64;
     return k <= 2048 && n * k / 1024 * batch <= 800;
@@ -101,8 +102,8 @@ inline Plan make_plan(int M, int N, int batch) {
     p.s_size = (int64_t)p.n * p.lds;
     // Few tiles and a long k leave compute units idle: enough parts to give
     // each one a tile (two side by side where one does not go round), no part below 512 deep.
-    // 8192 x 1024 (36 tiles): 337 us for the whole call in 7 parts, 361 in 8,
-    // 345 in 14; 2048 x 8192 (136 tiles): 887 in one, 757 in 3.
+    // 8192 x 1024 (36 tiles): 344 us for the whole call in 7 parts, 350 in 14, 466
+    // in one; 1024 x 8192 348, 365, 605; 2048 x 8192 (136 tiles) 796 in 3, 854 in 7, 936 in one.
     p.splits = 1;
     p.kc = p.k;
     const int64_t tiles = lower_tiles(p.n, kGramTile) * batch;

@@ -91,8 +91,9 @@ enum gemm_status {
                                    other than 0 or 1, a negative batch,
                                    splits or workspace size, or a stride
                                    outside [0, 2^48)                         */
-    GEMM_ERR_WORKSPACE = -8,    /* gemm_splitk: workspace NULL or smaller
-                                   than gemm_splitk_workspace_size           */
+    GEMM_ERR_WORKSPACE = -8,    /* gemm_splitk, gemm_streamk,
+                                   gemm_orthogonalize: workspace NULL or
+                                   smaller than the call's workspace size    */
     GEMM_ERR_SCRATCH = -9,      /* gemm_splitk_noalloc: the shape's partials
                                    (gemm_splitk_workspace_size) exceed
                                    DGT_GEMM_NOALLOC_SCRATCH_BYTES            */
@@ -382,9 +383,12 @@ int gemm_mx4(int M, int N, int K, float alpha, const uint8_t* A, int lda,
 /* The same with 16-bit A (GEMM_DTYPE_BF16 or GEMM_DTYPE_F16, M x K, row pitch
  * lda elements, any alignment) against MX4 B: the products of a 16-bit and a
  * 4-bit value are exact and summed in fp32 (with BF16 A a weight of 2^128 or
- * more, which gemm_mx4_quantize never writes, counts as infinite).  For batches of up to some
- * hundred rows: from about 800 (BF16) or 300 (FP16) on, gemm_mx4_dequantize
- * and the dense product take less time, where there is room for the result. */
+ * more, which gemm_mx4_quantize never writes, counts as infinite).  For
+ * batches of up to some hundred rows: from about 800 (BF16) or 300 (FP16) rows on,
+ * gemm_mx4_dequantize and the dense product take less time, where there is
+ * room for the result.  A whose rows are not on 16-byte boundaries (K, or a
+ * padded pitch, not a multiple of 8) streams B once per 16 or 32 rows and takes
+ * 2 to 6 times as long from 8 rows on; a padded copy of A is faster. */
 int gemm_mx4_a16(int dtype, int M, int N, int K, float alpha, const uint16_t* A,
                  int lda, const uint8_t* B, int ldb, const uint8_t* SB, int ldsb,
                  float beta, float* C, int ldc, const float* bias, void* stream);
