@@ -18,10 +18,11 @@
 // result's own bf16 rounding costs.  X is therefore kept as two halves hi + lo
 // (22 bits) in every step; the products read hi, the term a X both.  What hi's
 // rounding E adds through the products reaches the weak directions only as (b S + c S S) E,
-// small where S is.  The result is normwise 1.7e-3 off for exact low rank and 1/i^2
-// spectra, 1.7 to 1.9e-3 for 1/i, 1.7 to 2.5e-3 for normal values or a floor of them, where the
-// roundings of S and B count too (matrices of 200 to 4096, five steps); with few rows these
-// average less: 2.8e-3 for 64 x 2^24, 5.7e-3 for one row.
+// small where S is.  B is largest on its diagonal; what its rounding takes there is kept in
+// fp32 and added in the update, times hi like the rest of B's row (one row 5000 long:
+// 3.3e-3 without, 2.3e-3 with it; 48 x 2600 3.1e-3, 2.2e-3).  The result is normwise 1.7e-3 off for
+// exact low rank and 1/i^2 spectra, 1.7 to 1.8e-3 for 1/i, 1.7 to 2.5e-3 for normal
+// values or a floor of them, where the roundings of S and B count too (1 to 4096 rows, five steps).
 //
 // FP16's range: |X| <= |X|_2, about 1, but its elements are near
 // 1/sqrt(max(M, N)) and the Gram matrix's smaller still, so X is held times
@@ -205,15 +206,19 @@ __device__ __forceinline__ TileIdx lower_tile(int64_t per_problem) {
 }
 
 // A symmetric n x n product's tile: OUT <- f1 * sums (+ f2 * D), and mirrored
-// off the diagonal; D is OUT's layout.
+// off the diagonal; D is OUT's layout.  With D, diag <- what rounding took from
+// OUT's diagonal.
 template <int R, bool TA, bool TB, bool kEdge, bool kTail, bool kAdd>
 __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void symmetric_kernel(
-    GemmParams p, int64_t tiles, _Float16* out, const _Float16* add, int64_t ld, int64_t size,
-    float f1, float f2) {
+    GemmParams p, int64_t tiles, _Float16* out, const _Float16* add, float* diag, int64_t ld,
+    int64_t size, float f1, float f2) {
     const TileIdx tile = lower_tile(tiles);
     select_problem(p, tile.z);
     out += tile.z * size;
-    if constexpr (kAdd) add += tile.z * size;
+    if constexpr (kAdd) {
+        add += tile.z * size;
+        diag += (int64_t)tile.z * p.M;
+    }
     const int m0 = tile.bm * R, n0 = tile.bn * R;
     dma_tile<In::F16, R, TA, TB, kEdge, kTail>(
         p, m0, n0, nullptr, [&](const auto& acc, int wm, int wn, int lane, uint8_t* mem) {
@@ -247,14 +252,24 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void symmetric_kernel(
                     halfx8 o;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        v[e] = kAdd ? f2 * (float)d[ti & 1][i][e] + f1 * v[e] : f1 * v[e];
+                        v[e] = kAdd ? fmaf(f2, (float)d[ti & 1][i][e], f1 * v[e]) : f1 * v[e];
                         o[e] = (_Float16)v[e];
                     }
                     if (kAdd && m0 != n0) chunk.set_row8(r, c, v);  // for the mirrored pieces
                     if (!kEdge || (row < p.M && col < p.N))
                         *reinterpret_cast<halfx8*>(out + row * ld + col) = o;
                 }
-                if (m0 == n0) continue;
+                if (m0 == n0) {
+                    if constexpr (kAdd) {  // one lane an element, the same operations as above
+                        const int row = row0 + 32 * ti + lane;
+                        if (wm == wn && lane < 32 && (!kEdge || row < p.M)) {
+                            const float v = fmaf(f2, (float)add[row * ld + row],
+                                                 f1 * chunk.mem[Ch::at(lane, 32 * ti + lane)]);
+                            diag[row] = v - (float)(_Float16)v;
+                        }
+                    }
+                    continue;
+                }
                 if constexpr (kAdd) Ch::fence();
 #pragma unroll
                 for (int i = 0; i < Ch::PIECES; ++i) {
@@ -272,10 +287,13 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void symmetric_kernel(
         });
 }
 
-// X' = a (hi + lo) + f * sums: two halves, or (kLast) the result in bf16.
+// X' = a (hi + lo) + f * (sums + diag hi): two halves, or (kLast) the result in
+// bf16; diag holds the rest of B's diagonal, of the rows of X (of its columns for a tall
+// X, whose B stands on the right).
 struct Update {
     const _Float16 *hi, *lo;
     _Float16 *hi2, *lo2;
+    const float* diag;
     int64_t ldx, x_size;
     float a, f;
     uint16_t* O;
@@ -310,6 +328,17 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams
                 }
             };
             fetch(0);
+            // The diagonal's rest.  Of the rows: one per lane, taken from the lane
+            // that has it; of the columns: a lane's eight are the same in every piece.
+            constexpr int ND = TB ? 8 : R / 128;
+            static_assert(64 % Ch::GROUPS == 0, "a lane's columns");
+            const float* diag = u.diag + (int64_t)tile.z * (TB ? p.N : p.M);
+            float d[ND];
+#pragma unroll
+            for (int j = 0; j < ND; ++j) {
+                const int at = TB ? col0 + Ch::col(0, lane) + j : row0 + 64 * j + lane;
+                d[j] = at < (TB ? p.N : p.M) ? diag[at] : 0.0f;
+            }
 #pragma unroll
             for (int ti = 0; ti < Geo<R>::TM; ++ti) {
                 if (ti + 1 < Geo<R>::TM) fetch(ti + 1);
@@ -320,11 +349,15 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void update_kernel(GemmParams
                     const int row = row0 + 32 * ti + r, col = col0 + c;
                     float x[8];
                     chunk.row8(r, c, x);
+                    const float dr = TB ? 0.0f : __shfl(d[TB ? 0 : ti / 2], 32 * (ti & 1) + r);
                     if (kEdge && (row >= p.M || col >= p.N)) continue;
                     const int64_t at = xz + (int64_t)row * u.ldx + col;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = u.a * ((float)h[ti & 1][i][e] + (float)l[ti & 1][i][e]) + u.f * x[e];
+                    for (int e = 0; e < 8; ++e) {
+                        const float hi = (float)h[ti & 1][i][e];
+                        x[e] = u.a * (hi + (float)l[ti & 1][i][e]) +
+                               u.f * fmaf(TB ? d[TB ? e : 0] : dr, hi, x[e]);
+                    }
                     if constexpr (kLast) {
                         bf16x8 o;
 #pragma unroll
@@ -449,15 +482,15 @@ bool use128(int64_t t256, int64_t t128) {
 }
 
 template <bool TA, bool TB, bool kAdd>
-hipError_t symmetric(const GemmParams& g, _Float16* out, const _Float16* add, int64_t ld,
-                     int64_t size, float f1, float f2, hipStream_t s) {
+hipError_t symmetric(const GemmParams& g, _Float16* out, const _Float16* add, float* diag,
+                     int64_t ld, int64_t size, float f1, float f2, hipStream_t s) {
     auto go = [&](auto rc) {
         constexpr int R = decltype(rc)::value;
         const int64_t tiles = lower_tiles(g.M, R);
         if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
         auto launch = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, dim3((unsigned)tiles, g.batch), dim3(NT), 0, s, g, tiles,
-                               out, add, ld, size, f1, f2);
+                               out, add, diag, ld, size, f1, f2);
             return hipGetLastError();
         };
         if (g.K % (BK * NSTAGE) != 0) return launch(symmetric_kernel<R, TA, TB, true, true, kAdd>);
@@ -494,7 +527,7 @@ hipError_t update(const GemmParams& g, const Update& u, bool last, hipStream_t s
 template <bool TA, bool TB>
 hipError_t gram(const Plan& p, const GemmParams& g, _Float16* S, float f, uint8_t* ws,
                 hipStream_t s) {
-    if (p.splits == 1) return symmetric<TA, TB, false>(g, S, nullptr, p.lds, p.s_size, f, 0.0f, s);
+    if (p.splits == 1) return symmetric<TA, TB, false>(g, S, nullptr, nullptr, p.lds, p.s_size, f, 0.0f, s);
     float* partial = reinterpret_cast<float*>(ws + p.partial);
     const unsigned tiles = (unsigned)lower_tiles(p.n, kGramTile);
     const dim3 grid(tiles * p.splits * p.batch);  // a few hundred at most (make_plan)
@@ -546,12 +579,14 @@ hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
     _Float16* hi[2] = {half(p.hi[0]), half(p.hi[1])};
     _Float16* lo[2] = {half(p.lo[0]), half(p.lo[1])};
     _Float16 *S = half(p.gram), *B = half(p.poly);
+    float* diag = reinterpret_cast<float*>(c.ws + p.diag);
     hipError_t e = c.t == In::F32    ? init<In::F32>(p, c, hi[0], lo[0], s)
                    : c.t == In::BF16 ? init<In::BF16>(p, c, hi[0], lo[0], s)
                                      : init<In::F16>(p, c, hi[0], lo[0], s);
     const bool tall = p.M > p.N;
     const float xs = std::ldexp(1.0f, scale_exp(p.k));
     Update u = {};
+    u.diag = diag;
     u.ldx = p.ldx; u.x_size = p.x_size;
     u.a = c.a; u.f = 1.0f / kPolyScale;
     u.O = c.O; u.ldo = c.ldo; u.stride_o = c.stride_o;
@@ -565,7 +600,7 @@ hipError_t launch(const Plan& p, const Call& c, hipStream_t s) {
         e = tall ? gram<true, false>(p, g, S, fs, c.ws, s) : gram<false, true>(p, g, S, fs, c.ws, s);
         if (e != hipSuccess) return e;
         g = operands(p, p.n, p.n, p.n, S, p.lds, p.s_size, S, p.lds, p.s_size);
-        e = symmetric<false, true, true>(g, B, S, p.lds, p.s_size,
+        e = symmetric<false, true, true>(g, B, S, diag, p.lds, p.s_size,
                                          c.c * (kPolyScale / (kGramScale * kGramScale)),
                                          c.b * (kPolyScale / kGramScale), s);
         if (e != hipSuccess) return e;

@@ -13,7 +13,8 @@
 // multiples of 64; products of zero rows are zero, so the padding stays zero by
 // itself and nothing is masked.
 //
-// Precision as in k_orth.hip: X = hi + lo, products read hi, a X both.
+// Precision as in k_orth.hip: X = hi + lo, products read hi, a X both; what
+// rounding takes from B's diagonal is added to the update in fp32.
 #include "orth.hpp"
 
 namespace dgt {
@@ -69,10 +70,11 @@ struct Out {
     _Float16* a;        // Gram: S; Poly: B; Update: x (row-major)
     _Float16 *at, *lo;  // Update: xt and lo
     const _Float16 *prev, *prev_lo;  // Poly: S; Update, Last: xt and lo of X
+    float* diag;        // what rounding took from B's diagonal (n64 floats)
     uint16_t* O;        // Last
     int64_t ldo, stride_o;
     int M, N;
-    float f, g;         // Gram: f * sums; Poly: g * S + f * sums; Update: g * X + f * sums
+    float f, g;         // Gram: f * sums; Poly: g * S + f * sums; Update: g * X + f * (sums + diag x)
     float out_scale;
 };
 
@@ -124,12 +126,17 @@ __global__ __launch_bounds__(64 * NW) void small_product_kernel(const _Float16* 
     for (int w = 1; w < NW; ++w) sum += part[w][q][lane];
     const int m = m0 + 8 * q + 4 * (lane >> 5), n = n0 + (lane & 31);
     const int64_t t = z * size_out + (int64_t)n * rows + m;  // 4 neighbours of the transposed layout
+    float* diag = o.diag + z * rows;
     if constexpr (K == Kind::Gram || K == Kind::Poly) {  // symmetric: stored transposed
         halfx4 v;
         if constexpr (K == Kind::Poly) {
             const halfx4 s = *reinterpret_cast<const halfx4*>(o.prev + t);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = (_Float16)(o.g * (float)s[r] + o.f * sum[r]);
+            for (int r = 0; r < 4; ++r) {
+                const float b = o.g * (float)s[r] + o.f * sum[r];
+                v[r] = (_Float16)b;
+                if (m + r == n) diag[n] = b - (float)v[r];
+            }
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = (_Float16)(o.f * sum[r]);
@@ -138,9 +145,11 @@ __global__ __launch_bounds__(64 * NW) void small_product_kernel(const _Float16* 
     } else {
         const halfx4 h = *reinterpret_cast<const halfx4*>(o.prev + t);
         const halfx4 l = *reinterpret_cast<const halfx4*>(o.prev_lo + t);
+        const floatx4 d = *reinterpret_cast<const floatx4*>(diag + m);
         float x[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = o.g * ((float)h[r] + (float)l[r]) + o.f * sum[r];
+        for (int r = 0; r < 4; ++r)
+            x[r] = o.g * ((float)h[r] + (float)l[r]) + o.f * fmaf(d[r], (float)h[r], sum[r]);
         if constexpr (K == Kind::Update) {
             halfx4 nh, nl;
 #pragma unroll
@@ -208,6 +217,7 @@ hipError_t launch_small(const SmallPlan& p, const Call& c, hipStream_t s) {
         const int r = i & 1, w = 1 - r;
         const _Float16 *x = half(p.x[r]), *xt = half(p.xt[r]);
         Out o = {};
+        o.diag = reinterpret_cast<float*>(c.ws + p.diag);
         o.a = S;
         o.f = kGramScale / (xs * xs);
         e = product<Kind::Gram>(p, tall, x, x, p.x_size, p.x_size, p.s_size, p.n64, p.n64, p.k64, o, s);

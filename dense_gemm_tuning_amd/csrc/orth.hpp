@@ -27,7 +27,8 @@ inline int norm_parts(int M, int N) {
 // Workspace of a batch of M x N matrices, byte offsets from its start.  X is
 // kept as two FP16 halves (hi + lo), twice (a step reads one copy and writes
 // the other); S and B are the n x n Gram matrix and step polynomial, n the
-// smaller dimension and k the larger.  Rows are padded to 64 elements (128 bytes).
+// smaller dimension and k the larger; diag is what rounding to FP16 took from
+// B's diagonal (n floats).  Rows are padded to 64 elements (128 bytes).
 struct Plan {
     int M, N, batch, n, k;
     int64_t ldx, lds;           // elements
@@ -35,7 +36,7 @@ struct Plan {
     // The Gram matrix's sums over k in `splits` parts of kc (the last one
     // shorter) of tiles of kGramTile, when more than one part is worthwhile.
     int splits, kc;
-    int64_t hi[2], lo[2], gram, poly, partial, parts, bytes;
+    int64_t hi[2], lo[2], gram, poly, diag, partial, parts, bytes;
 };
 
 // Small matrices (k_orth_small.hip): every matrix padded with zeros to
@@ -44,7 +45,7 @@ struct SmallPlan {
     int M, N, batch, n, k;      // n <= k: a tall G is taken transposed
     int n64, k64;
     int64_t x_size, s_size;     // elements of one matrix
-    int64_t x[2], xt[2], lo[2], gram, poly, parts, bytes;
+    int64_t x[2], xt[2], lo[2], gram, poly, diag, parts, bytes;
 };
 
 // Whether a call takes them: products whose 32 x 32 tiles, a workgroup each,
@@ -80,6 +81,7 @@ inline SmallPlan make_small_plan(int M, int N, int batch) {
     }
     p.gram = take(batch * p.s_size * 2);
     p.poly = take(batch * p.s_size * 2);
+    p.diag = take((int64_t)batch * p.n64 * 4);
     p.bytes = at;
     return p;
 }
@@ -126,6 +128,7 @@ inline Plan make_plan(int M, int N, int batch) {
     }
     p.gram = take(batch * p.s_size * 2);
     p.poly = take(batch * p.s_size * 2);
+    p.diag = take((int64_t)batch * p.n * 4);
     p.partial = take(p.splits > 1 ? tiles * p.splits * kGramTile * kGramTile * 4 : 0);
     p.bytes = at;
     return p;

@@ -407,12 +407,10 @@ int gemm_mx4_a16(int dtype, int M, int N, int K, float alpha, const uint16_t* A,
  * O as raw bf16 bits (ldo, stride_o).  The norm is summed in 64 bits.  The
  * products take FP16 operands (scaled by powers of two into its range) and
  * sum in fp32; X itself is carried in two FP16 halves of together 22 bits,
- * and the term a*X uses both.  Normwise the result of five steps with the
- * usual coefficients differs from the exact iteration by 1.7e-3 (low rank,
- * fast falling spectra) to 2.5e-3 (normal values) from some hundred rows and columns
- * on, its own rounding to bf16 being 1.7e-3 of that; with fewer the
- * roundings of S and of the polynomial average less (2.8e-3 at 64 rows, up to
- * 6e-3 at one).  Every intermediate stays in range
+ * and the term a*X uses both; the diagonal of b*S + c*S*S keeps 32 bits.
+ * Normwise the result of five steps with the usual coefficients differs from
+ * the exact iteration by 1.7e-3 (low rank, fast falling spectra) to 2.5e-3
+ * (normal values, single rows), of which its own rounding to bf16 is 1.7e-3.  Every intermediate stays in range
  * while the iterates' singular values t do below 4 with
  * |b*t^2 + c*t^4| below 60.  A matrix holding an infinity or a NaN gives
  * NaN, and so does a zero matrix with eps = 0; neither touches the other

@@ -1,7 +1,8 @@
 """Newton-Schulz orthogonalisation in 64 bits on any device: the plain
 iteration, and the same with the roundings gemm_orthogonalize documents (FP16
 operands of every product, scaled by powers of two; X in two FP16 halves, of
-which the products read the first and the term a*X both)."""
+which the products read the first and the term a*X both; the polynomial's
+diagonal in 32 bits)."""
 
 import math
 
@@ -60,8 +61,9 @@ def rounded(G, steps=5, a=COEF[0], b=COEF[1], c=COEF[2], eps=1e-7):
         hi = half(X)
         lo = half(X - hi)
         S = half(4096.0 / scale ** 2 * hi.mm(hi.t().contiguous()))
-        B = half(1024.0 / 4096.0 * b * S + 1024.0 / 4096.0 ** 2 * c * S.mm(S))
-        X = a * (hi + lo) + B.mm(hi) / 1024.0
+        B = 1024.0 / 4096.0 * b * S + 1024.0 / 4096.0 ** 2 * c * S.mm(S)
+        rest = (B - half(B)).diagonal()[:, None]
+        X = a * (hi + lo) + (half(B).mm(hi) + rest * hi) / 1024.0
     return (X.t() if tall else X) / scale
 
 
