@@ -57,7 +57,20 @@ EXPORTS = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_f32_variant", "gemm_bf16_v
            "gemm_streamk", "gemm_streamk_workspace_size", "gemm_select_variant",
            "gemm_status_string", "gemm_abi_version", "gemm_mx4_code_pitch",
            "gemm_mx4_scale_pitch", "gemm_mx4_quantize", "gemm_mx4_dequantize", "gemm_mx4",
-           "gemm_mx4_a16", "gemm_orthogonalize", "gemm_orthogonalize_workspace_size")
+           "gemm_mx4_a16", "gemm_orthogonalize", "gemm_orthogonalize_workspace_size",
+           "gemm_gated", "gemm_gated_grad", "gemm_gated_grad_workspace_size", "gemm_w4_quantize",
+           "gemm_w4_dequantize", "gemm_w4_a16", "gemm_w4_gated")
+
+# enum gemm_activation
+ACT_SILU = 0
+ACT_GELU = 1
+ACT_GELU_TANH = 2
+ACT_RELU = 3
+ACT_SIGMOID = 4
+ACT_IDENTITY = 5
+ACTIVATIONS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU,
+               "sigmoid": ACT_SIGMOID, "identity": ACT_IDENTITY}
+GATED_MAX_DIM = 1 << 28  # DGT_GEMM_GATED_MAX_DIM
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
@@ -128,6 +141,20 @@ def _load() -> ctypes.CDLL:
                                            p]
         lib.gemm_orthogonalize_workspace_size.restype = i64
         lib.gemm_orthogonalize_workspace_size.argtypes = [i, i, i]
+        lib.gemm_gated.restype = i
+        lib.gemm_gated.argtypes = [i] * 5 + [p, i, p, i, p, i, p, p, p, i, p, i, p, i, p]
+        lib.gemm_gated_grad.restype = i
+        lib.gemm_gated_grad.argtypes = [i] * 5 + [p, i] * 7 + [p, p, p, i64, p]
+        lib.gemm_gated_grad_workspace_size.restype = i64
+        lib.gemm_gated_grad_workspace_size.argtypes = [i, i]
+        lib.gemm_w4_quantize.restype = i
+        lib.gemm_w4_quantize.argtypes = [i] * 5 + [p, i] * 4 + [p]
+        lib.gemm_w4_dequantize.restype = i
+        lib.gemm_w4_dequantize.argtypes = [i] * 5 + [p, i] * 4 + [p]
+        lib.gemm_w4_a16.restype = i
+        lib.gemm_w4_a16.argtypes = [i] * 6 + [f, p, i, p, i, p, i, p, i, f, p, i, p, p]
+        lib.gemm_w4_gated.restype = i
+        lib.gemm_w4_gated.argtypes = [i] * 7 + [p, i] * 4 + [p, p, p, i, p]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [i]
         lib.gemm_abi_version.restype = i
@@ -260,6 +287,47 @@ def gemm_orthogonalize(dtype, M, N, G, ldg, stride_g, O, ldo, stride_o, batch, s
 
 def gemm_orthogonalize_workspace_size(M, N, batch) -> int:
     return _load().gemm_orthogonalize_workspace_size(M, N, batch)
+
+
+def gemm_gated(dtype, act, M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, bias_g, bias_u, H, ldh, G=0, ldg=0,
+               U=0, ldu=0, stream=0) -> int:
+    return _load().gemm_gated(int(dtype), int(act), M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, bias_g,
+                              bias_u, H, ldh, G, ldg, U, ldu, stream)
+
+
+def gemm_gated_grad(dtype, act, M, N, K, dY, lddy, Wd, ldw, G, ldg, U, ldu, dG, lddg, dU, lddu, H=0,
+                    ldh=0, dbias_g=0, dbias_u=0, workspace=0, workspace_bytes=0, stream=0) -> int:
+    return _load().gemm_gated_grad(int(dtype), int(act), M, N, K, dY, lddy, Wd, ldw, G, ldg, U, ldu,
+                                   dG, lddg, dU, lddu, H, ldh, dbias_g, dbias_u, workspace,
+                                   int(workspace_bytes), stream)
+
+
+def gemm_gated_grad_workspace_size(M, N) -> int:
+    return _load().gemm_gated_grad_workspace_size(M, N)
+
+
+def gemm_w4_quantize(dtype, group, scale_dtype, M, K, X, ldx, Q, ldq, S, lds, Z=0, ldz=0,
+                     stream=0) -> int:
+    return _load().gemm_w4_quantize(int(dtype), int(group), int(scale_dtype), M, K, X, ldx, Q, ldq,
+                                    S, lds, Z, ldz, stream)
+
+
+def gemm_w4_dequantize(dtype, group, scale_dtype, M, K, Q, ldq, S, lds, Z, ldz, Y, ldy,
+                       stream=0) -> int:
+    return _load().gemm_w4_dequantize(int(dtype), int(group), int(scale_dtype), M, K, Q, ldq, S,
+                                      lds, Z, ldz, Y, ldy, stream)
+
+
+def gemm_w4_a16(dtype, group, scale_dtype, M, N, K, alpha, A, lda, Q, ldq, S, lds, Z, ldz, beta, C,
+                ldc, bias=0, stream=0) -> int:
+    return _load().gemm_w4_a16(int(dtype), int(group), int(scale_dtype), M, N, K, alpha, A, lda, Q,
+                               ldq, S, lds, Z, ldz, beta, C, ldc, bias, stream)
+
+
+def gemm_w4_gated(dtype, act, group, scale_dtype, M, N, K, X, ldx, Q, ldq, S, lds, Z, ldz, bias_g,
+                  bias_u, H, ldh, stream=0) -> int:
+    return _load().gemm_w4_gated(int(dtype), int(act), int(group), int(scale_dtype), M, N, K, X,
+                                 ldx, Q, ldq, S, lds, Z, ldz, bias_g, bias_u, H, ldh, stream)
 
 
 def gemm_status_string(status: int) -> str:
@@ -741,18 +809,260 @@ def orthogonalize(G, O, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     if need < 0:
         return need
     if workspace is None:
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
-        else:  # in that stream's order, so that a later call cannot get it too early
-            if hasattr(stream, "cuda_stream"):
-                on = stream
-            elif stream == 0:  # ExternalStream takes 0 for "any stream of the pool"
-                on = torch.cuda.default_stream(O.device)
-            else:
-                on = torch.cuda.ExternalStream(stream, device=O.device)
-            with torch.cuda.stream(on):
-                workspace = torch.empty(need, dtype=torch.uint8, device=O.device)
+        workspace = _workspace(need, O.device, stream)
     a, b, c = (float(x) for x in coefficients)
     return _call_on(index, stream, _load().gemm_orthogonalize, dtype, M, N, G2.data_ptr(), ldg,
                     sg, O2.data_ptr(), ldo, so, batch, int(steps), a, b, c, float(eps),
                     workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _act_code(act):
+    code = ACTIVATIONS.get(act) if isinstance(act, str) else act
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return int(code)
+
+
+def _code16(t, name):
+    if t.dtype is (_torch or _use_torch()).float32:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    return _float_code(t, name)
+
+
+def _matrix16(t, name, dtype, shape):
+    """(pointer, pitch) of a 16-bit tensor of the call's type and this shape."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} as the call's other tensors, got {t.dtype}")
+    rows, cols, pitch = _matrix(t, name)
+    if rows != shape[0] or cols != shape[1]:
+        raise ValueError(f"shape mismatch: {name} {(rows, cols)}, expected {shape}")
+    return t.data_ptr(), pitch
+
+
+def _vector(t, name, N):
+    """The pointer of N contiguous fp32 values (None: null)."""
+    if t is None:
+        return 0
+    if t.dtype is not _torch.float32 or t.dim() != 1 or t.shape[0] != N:
+        raise ValueError(f"{name} must be float32 [N]")
+    if N > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def gated(X, Wg, Wu, H, act="silu", bias_g=None, bias_u=None, G=None, U=None, stream=None) -> int:
+    """H <- act(X*Wg^T + bias_g) * (X*Wu^T + bias_u) (gemm_gated): the gated
+    projections of a feed-forward block in one kernel.
+
+    X is [M, K], Wg and Wu [N, K] (weights as a linear layer stores them; they may
+    be the row halves of one tensor), H [M, N], all bfloat16 or all float16,
+    row-major; the biases float32 [N] or None.  ``act`` is a name in ACTIVATIONS.
+    G and U, [M, N] like H, keep the two pre-activations for ``gated_grad`` (they may
+    be column halves of one tensor).  Returns the status code."""
+    dtype = _code16(X, "X")
+    M, K, ldx = _matrix(X, "X")
+    N = Wg.shape[0]
+    wg, ldwg = _matrix16(Wg, "Wg", X.dtype, (N, K))
+    wu, ldwu = _matrix16(Wu, "Wu", X.dtype, (N, K))
+    h, ldh = _matrix16(H, "H", X.dtype, (M, N))
+    g, ldg = (0, 0) if G is None else _matrix16(G, "G", X.dtype, (M, N))
+    u, ldu = (0, 0) if U is None else _matrix16(U, "U", X.dtype, (M, N))
+    bg, bu = _vector(bias_g, "bias_g", N), _vector(bias_u, "bias_u", N)
+    index = H.get_device()
+    _on_device(index, [(name, t) for name, t in (("X", X), ("Wg", Wg), ("Wu", Wu), ("H", H), ("G", G),
+                                                 ("U", U), ("bias_g", bias_g), ("bias_u", bias_u))
+                       if t is not None])
+    code = _act_code(act)
+    if M == 0 or N == 0:
+        return GEMM_OK
+    return _call_on(index, stream, _load().gemm_gated, dtype, code, M, N, K, X.data_ptr(), ldx, wg,
+                    ldwg, wu, ldwu, bg, bu, h, ldh, g, ldg, u, ldu)
+
+
+def gated_grad(dY, Wd, G, U, dG, dU, act="silu", H=None, dbias_g=None, dbias_u=None, workspace=None,
+               stream=None) -> int:
+    """The gradient at the gated projections (gemm_gated_grad) from dY [M, K], the
+    gradient of Y = H*Wd^T with Wd [K, N] as stored, and the G and U that ``gated`` kept:
+
+        dh = dY*Wd,  dG <- dh * U * act'(G),  dU <- dh * act(G)
+
+    and, where they are given, H <- act(G)*U again and the column sums of dG
+    and dU in dbias_g and dbias_u (float32 [N]).  All matrices are bfloat16 or all
+    float16, row-major, [M, N] but for dY and Wd; dG may be G and dU may be U.  With
+    dG and dU column halves of one tensor D and the weights row halves of one
+    tensor W, ``gemm(D, W, dX)`` and ``gemm(D, X, dW, trans_a=True)`` finish the
+    block's gradient.  ``workspace`` is only used for the bias gradients: a contiguous GPU tensor of
+    at least gemm_gated_grad_workspace_size bytes that no other call uses at the
+    same time; when None one is allocated here with torch, for the stream the
+    work runs on.  Returns the status code."""
+    torch = _torch or _use_torch()
+    dtype = _code16(dY, "dY")
+    M, K, lddy = _matrix(dY, "dY")
+    N = G.shape[1] if G.dim() == 2 else 0
+    wd, ldw = _matrix16(Wd, "Wd", dY.dtype, (K, N))
+    args = []
+    named = [("dY", dY), ("Wd", Wd)]
+    for name, t in (("G", G), ("U", U), ("dG", dG), ("dU", dU), ("H", H)):
+        if t is None and name == "H":
+            args += (0, 0)
+            continue
+        args += _matrix16(t, name, dY.dtype, (M, N))
+        named.append((name, t))
+    sums = [_vector(dbias_g, "dbias_g", N), _vector(dbias_u, "dbias_u", N)]
+    named += [(name, t) for name, t in (("dbias_g", dbias_g), ("dbias_u", dbias_u),
+                                        ("workspace", workspace)) if t is not None]
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    # of an empty batch only the sums are written
+    owner = next((t for t in (dG, dbias_g, dbias_u) if t is not None and t.numel() > 0), dG)
+    index = owner.get_device()
+    _on_device(index, named)
+    code = _act_code(act)
+    if N == 0 or (M == 0 and not any(sums)):
+        return GEMM_OK
+    if any(sums) and workspace is None and M > 0:
+        need = gemm_gated_grad_workspace_size(M, N)
+        if need < 0:
+            return need
+        workspace = _workspace(need, owner.device, stream)
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                                     workspace.numel() * workspace.element_size())
+    return _call_on(index, stream, _load().gemm_gated_grad, dtype, code, M, N, K, dY.data_ptr(), lddy,
+                    wd, ldw, *args, *sums, ws, ws_bytes)
+
+
+def _workspace(nbytes, device, stream):
+    """``nbytes`` of device memory in the stream's order, so that a later call
+    cannot get it too early."""
+    torch = _torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if hasattr(stream, "cuda_stream"):
+        on = stream
+    elif stream == 0:  # ExternalStream takes 0 for "any stream of the pool"
+        on = torch.cuda.default_stream(device)
+    else:
+        on = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(on):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def w4_empty(rows: int, K: int, group: int = 128, scale_dtype=None, zeros: bool = True,
+             device="cuda"):
+    """Uninitialised storage of a rows x K weight in 4 bits with a scale per
+    ``group`` (32, 64 or 128) consecutive k: (codes, scales, zero points), uint8,
+    ``scale_dtype`` (torch.float16, the default, or torch.bfloat16) and uint8, or
+    None for the zero points without ``zeros``."""
+    torch = _torch or _use_torch()
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    if not 0 <= K <= 2 * MX4_MAX_PITCH:
+        raise ValueError(f"K must be at most 2^25, got {K}")
+    n = (K + group - 1) // group
+    return (torch.empty(rows, gemm_mx4_code_pitch(K), dtype=torch.uint8, device=device),
+            torch.empty(rows, n, dtype=scale_dtype or torch.float16, device=device),
+            torch.empty(rows, n, dtype=torch.uint8, device=device) if zeros else None)
+
+
+def _weight4(Q, S, Z, rows, K, group):
+    """(scale type's code, [pointer, pitch of codes, scales, zero points]) of a
+    rows x K weight in 4 bits."""
+    scale = _code16(S, "S (scales)")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    cols, ldq = _bytes(Q, "Q (codes)", rows)
+    need = (K + 31) // 32 * 16
+    if cols < need:
+        raise ValueError(f"Q: {K} elements need rows of {need} code bytes, got {cols}")
+    n = (K + group - 1) // group
+    at = [Q.data_ptr(), ldq]
+    for name, t in (("S (scales)", S), ("Z (zero points)", Z)):
+        if t is None:
+            at += (0, 0)
+            continue
+        have, cols, pitch = _matrix(t, name)
+        if have != rows or cols != n:
+            raise ValueError(f"{name} must be [{rows}, {n}] for {K} elements in groups of {group}, "
+                             f"got {[have, cols]}")
+        at += (t.data_ptr(), pitch)
+    if Z is not None and Z.dtype is not _torch.uint8:
+        raise TypeError(f"Z (zero points) must be uint8, got {Z.dtype}")
+    return scale, at
+
+
+def _on_device4(index, Q, S, Z, named):
+    _on_device(index, [("Q", Q), ("S", S), *named] + ([] if Z is None else [("Z", Z)]))
+
+
+def quantize_w4(X, Q, S, Z=None, group: int = 128, stream=None) -> int:
+    """(Q, S, Z) <- X [rows, K] in 4 bits with a scale, and unless Z is None a zero
+    point, per ``group`` consecutive elements of a row (gemm_w4_quantize).  X is
+    float32, bfloat16 or float16, row-major; Q, S and Z as ``w4_empty`` makes them,
+    or views of wider storage.  Returns the status code."""
+    dtype = _float_code(X, "X")
+    M, K, ldx = _matrix(X, "X")
+    scale, at = _weight4(Q, S, Z, M, K, group)
+    index = Q.get_device()
+    _on_device4(index, Q, S, Z, [("X", X)])
+    if M == 0 or K == 0:
+        return GEMM_OK
+    return _call_on(index, stream, _load().gemm_w4_quantize, dtype, group, scale, M, K, X.data_ptr(),
+                    ldx, *at)
+
+
+def dequantize_w4(Q, S, Z, Y, group: int = 128, stream=None) -> int:
+    """Y [rows, K] <- the values of a weight in 4 bits (gemm_w4_dequantize), Y
+    float32, bfloat16 or float16, row-major.  Returns the status code."""
+    dtype = _float_code(Y, "Y")
+    M, K, ldy = _matrix(Y, "Y")
+    scale, at = _weight4(Q, S, Z, M, K, group)
+    index = Y.get_device()
+    _on_device4(index, Q, S, Z, [("Y", Y)])
+    if M == 0 or K == 0:
+        return GEMM_OK
+    return _call_on(index, stream, _load().gemm_w4_dequantize, dtype, group, scale, M, K, *at,
+                    Y.data_ptr(), ldy)
+
+
+def gemm_w4(A, Q, S, Z, C, group: int = 128, alpha: float = 1.0, beta: float = 0.0, bias=None,
+            stream=None) -> int:
+    """C <- alpha*A*W^T + beta*C + bias with W the [N, K] weight in 4 bits Q, S, Z
+    (Z None: zero points 8) and A [M, K] bfloat16 or float16 (gemm_w4_a16).  C is float32 [M, N],
+    row-major; bias None or float32 [N].  Returns the status code."""
+    if C.dtype is not (_torch or _use_torch()).float32:
+        raise TypeError("C must be float32")
+    dtype = _code16(A, "A")
+    M, N, ldc = _matrix(C, "C")
+    rows, K, lda = _matrix(A, "A")
+    if rows != M:
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, C {tuple(C.shape)}")
+    scale, at = _weight4(Q, S, Z, N, K, group)
+    bias_ptr = _vector(bias, "bias", N)
+    index = C.get_device()
+    _on_device4(index, Q, S, Z, [("A", A), ("C", C)] + ([] if bias is None else [("bias", bias)]))
+    if M == 0 or N == 0:
+        return GEMM_OK
+    return _call_on(index, stream, _load().gemm_w4_a16, dtype, group, scale, M, N, K, float(alpha),
+                    A.data_ptr(), lda, *at, float(beta), C.data_ptr(), ldc, bias_ptr)
+
+
+def gated_w4(X, Q, S, Z, H, act="silu", group: int = 128, bias_g=None, bias_u=None,
+             stream=None) -> int:
+    """H <- act(X*Wg^T + bias_g) * (X*Wu^T + bias_u) with the weight in 4 bits Q, S, Z
+    of 2N rows, Wg's and then Wu's (gemm_w4_gated).  X [M, K] and H [M, N] are both
+    bfloat16 or both float16, row-major; the biases float32 [N] or None.  Returns
+    the status code."""
+    dtype = _code16(X, "X")
+    M, K, ldx = _matrix(X, "X")
+    N = H.shape[1] if H.dim() == 2 else 0
+    h, ldh = _matrix16(H, "H", X.dtype, (M, N))
+    scale, at = _weight4(Q, S, Z, 2 * N, K, group)
+    bg, bu = _vector(bias_g, "bias_g", N), _vector(bias_u, "bias_u", N)
+    index = H.get_device()
+    _on_device4(index, Q, S, Z, [(name, t) for name, t in (("X", X), ("H", H), ("bias_g", bias_g),
+                                                           ("bias_u", bias_u)) if t is not None])
+    code = _act_code(act)
+    if M == 0 or N == 0:
+        return GEMM_OK
+    return _call_on(index, stream, _load().gemm_w4_gated, dtype, code, group, scale, M, N, K,
+                    X.data_ptr(), ldx, *at, bg, bu, h, ldh)

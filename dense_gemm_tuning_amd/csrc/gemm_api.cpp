@@ -456,16 +456,16 @@ int gemm_select_variant(int dtype, int trans_a, int trans_b, int M, int N, int K
 const char* gemm_status_string(int status) {
     switch (status) {
         case GEMM_OK: return "GEMM_OK: success";
-        case GEMM_ERR_DIM: return "GEMM_ERR_DIM: M, N or K is negative, or past an MX4 or orthogonalisation limit";
+        case GEMM_ERR_DIM: return "GEMM_ERR_DIM: M, N or K is negative, or past an MX4, gated, W4 or orthogonalisation limit";
         case GEMM_ERR_LD: return "GEMM_ERR_LD: leading dimension too small";
         case GEMM_ERR_NULL: return "GEMM_ERR_NULL: null pointer for a non-empty operand";
         case GEMM_ERR_OVERLAP: return "GEMM_ERR_OVERLAP: C overlaps A or B";
         case GEMM_ERR_VARIANT: return "GEMM_ERR_VARIANT: variant unknown or unsupported for this shape";
         case GEMM_ERR_LAUNCH: return "GEMM_ERR_LAUNCH: the HIP runtime rejected the launch";
-        case GEMM_ERR_ARG: return "GEMM_ERR_ARG: unknown dtype or transpose flag, negative batch, splits or size, or stride out of range";
+        case GEMM_ERR_ARG: return "GEMM_ERR_ARG: unknown dtype, transpose flag, activation or group, negative batch, splits or size, or stride out of range";
         case GEMM_ERR_WORKSPACE: return "GEMM_ERR_WORKSPACE: workspace missing or smaller than the call's workspace size";
         case GEMM_ERR_SCRATCH: return "GEMM_ERR_SCRATCH: gemm_splitk_noalloc: the partials (slices x M x N x 4 bytes) exceed the library's fixed scratch of DGT_GEMM_NOALLOC_SCRATCH_BYTES";
-        case GEMM_ERR_ALIGN: return "GEMM_ERR_ALIGN: MX4 codes or scales, or a workspace, not on 16-byte boundaries (base and row pitch)";
+        case GEMM_ERR_ALIGN: return "GEMM_ERR_ALIGN: MX4 codes or scales, W4 codes, or a workspace, not on 16-byte boundaries (base and row pitch)";
         default: return "unknown gemm status";
     }
 }

@@ -1,0 +1,319 @@
+// k_gated_regs.hip -- the gated projections and their gradient for operands of
+// any alignment, staged through registers.
+//
+// Tile 128 rows by 128 products, 2 x 2 wavefronts of 64 x 64 (2 x 2
+// v_mfma_f32_32x32x16).  Forward: a wavefront's 64 products are 32 of the gate and
+// the same 32 columns of the other projection, so that both pre-activations of
+// an element end up in one lane.  Gradient: 64 columns of dh.
+//
+// K advances in slices of 64, the next one loaded into registers while the
+// current one is multiplied from LDS (two buffers, one barrier a slice).  A
+// slice that lies inside K is loaded 16 bytes at a time from wherever a row
+// starts (the GPU runs with unaligned access enabled), rows past the end
+// re-reading the last one (their products are not stored); the last, partial slice
+// and column blocks that cross N are gathered element by element with zeros outside.
+// Chunk q (8 k) of row r sits at q ^ ((r ^ r>>3) & 7).
+#include "gated.hpp"
+
+namespace dgt {
+namespace gated {
+
+namespace {
+
+constexpr int BM = 128, BB = 128, BK = 64, NT = 256, CPR = BK / 8;
+
+__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+__device__ __forceinline__ u32x4 load16(const uint16_t* src) {
+    u32x4 v;
+    __builtin_memcpy(&v, src, 16);
+    return v;
+}
+
+// Elements [at, at + 8) of a row, zeros from `limit` on.
+__device__ __forceinline__ u32x4 gather8(const uint16_t* row, int at, int limit) {
+    u32x4 v;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t lo = at + 2 * d < limit ? row[at + 2 * d] : 0u;
+        const uint32_t hi = at + 2 * d + 1 < limit ? row[at + 2 * d + 1] : 0u;
+        v[d] = lo | (hi << 16);
+    }
+    return v;
+}
+
+// An operand stored with k contiguous: lane chunk i is staged row tid/8 + 32*i,
+// chunk tid%8.
+struct Rows {
+    const uint16_t* row[4];
+    u32x4 v[4];
+    __device__ void load(int k0, int K, int q) {
+        const int at = k0 + 8 * q;
+        if (k0 + BK <= K) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = load16(row[i] + at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = gather8(row[i], at, K);
+        }
+    }
+    __device__ void store(u32x4* dst, int tid) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (tid >> 3) + 32 * i;
+            dst[r * CPR + ((tid & 7) ^ swz(r))] = v[i];
+        }
+    }
+};
+
+// An operand stored K x N: the lane takes k-rows 4*(tid/16) .. +3, columns
+// 8*(tid%16) .. +7 of the tile, and writes them as eight columns of 4 k.
+struct Columns {
+    u32x4 v[4];
+    __device__ void load(const uint16_t* W, int64_t ld, int n0, int N, int k0, int K, int tid) {
+        const int col = n0 + 8 * (tid & 15), k = k0 + 4 * (tid >> 4);
+        if (k0 + BK <= K && n0 + BB <= N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = load16(W + (int64_t)(k + i) * ld + col);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = gather8(W + (int64_t)min(k + i, K - 1) * ld, col, k + i < K ? N : 0);
+        }
+    }
+    __device__ void store(u32x4* dst, int tid) const {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const int k = 4 * (tid >> 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int n = 8 * (tid & 15) + j;
+            u32x2 c;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t a = v[2 * e][j / 2], b = v[2 * e + 1][j / 2];
+                c[e] = j % 2 ? (a >> 16) | (b & 0xffff0000u) : (a & 0xffffu) | (b << 16);
+            }
+            *(reinterpret_cast<u32x2*>(dst + n * CPR + ((k / 8) ^ swz(n))) + (k / 4) % 2) = c;
+        }
+    }
+};
+
+struct Place {
+    int lane, wm, wn, h, c;  // h: half of the wavefront, c: its column
+};
+
+// The sums of one tile; load and store move slice k0 of both operands.
+template <In T, typename Load, typename Store>
+__device__ __forceinline__ void products(int K, const u32x4 (*As)[BM * CPR],
+                                         const u32x4 (*Bs)[BB * CPR], const Place& at, Load&& load,
+                                         Store&& store, floatx16 (&acc)[2][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    const int nk = K / BK + (K % BK != 0);
+    if (nk == 0) return;
+    load(0);
+    store(0);
+    __syncthreads();
+    for (int t = 0; t < nk; ++t) {
+        const int buf = t & 1;
+        if (t + 1 < nk) load((t + 1) * BK);
+#pragma unroll
+        for (int s = 0; s < BK / 16; ++s) {
+            const int q = 2 * s + at.h;
+            u32x4 a[2], b[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int ra = at.wm * 64 + i * 32 + at.c, rb = at.wn * 64 + i * 32 + at.c;
+                a[i] = As[buf][ra * CPR + (q ^ swz(ra))];
+                b[i] = Bs[buf][rb * CPR + (q ^ swz(rb))];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16<T>(a[i], b[j], acc[i][j]);
+        }
+        if (t + 1 < nk) store(buf ^ 1);
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ Place place() {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    return Place{lane, wave >> 1, wave & 1, lane >> 5, lane & 31};
+}
+
+// Row of register r of an MFMA tile (32x32 accumulator layout).
+__device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+
+template <In T>
+__global__ __launch_bounds__(NT, 2) void forward_regs_kernel(Forward p, int tiles_n) {
+    __shared__ u32x4 As[2][BM * CPR], Bs[2][BB * CPR];
+    const int tid = threadIdx.x;
+    const Place at = place();
+    const int m0 = (int)(blockIdx.x / (unsigned)tiles_n) * BM;
+    const int n0 = (int)(blockIdx.x % (unsigned)tiles_n) * (BB / 2);
+    Rows ra, rb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 3) + 32 * i;
+        ra.row[i] = p.X + (int64_t)min(m0 + r, p.M - 1) * p.ldx;
+        const int64_t n = min(n0 + 32 * (r / 64) + r % 32, p.N - 1);
+        rb.row[i] = (r / 32) % 2 ? p.Wu + n * p.ldwu : p.Wg + n * p.ldwg;
+    }
+    floatx16 acc[2][2];
+    products<T>(
+        p.K, As, Bs, at,
+        [&](int k0) {
+            ra.load(k0, p.K, tid & 7);
+            rb.load(k0, p.K, tid & 7);
+        },
+        [&](int buf) {
+            ra.store(As[buf], tid);
+            rb.store(Bs[buf], tid);
+        },
+        acc);
+    const int col = n0 + 32 * at.wn + at.c;
+    if (col >= p.N) return;
+    const float bg = p.bg ? p.bg[col] : 0.0f, bu = p.bu ? p.bu[col] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int64_t row = m0 + 64 * at.wm + 32 * i + acc_row(r, at.h);
+            if (row >= p.M) continue;
+            const float g = acc[i][0][r] + bg, u = acc[i][1][r] + bu;
+            p.H[row * p.ldh + col] = to_bits<T>(act_of(p.act, g) * u);
+            if (p.G) p.G[row * p.ldg + col] = to_bits<T>(g);
+            if (p.U) p.U[row * p.ldu + col] = to_bits<T>(u);
+        }
+}
+
+template <In T>
+__global__ __launch_bounds__(NT, 2) void grad_regs_kernel(Grad p, int tiles_n) {
+    __shared__ u32x4 As[2][BM * CPR], Bs[2][BB * CPR];
+    const int tid = threadIdx.x;
+    const Place at = place();
+    const int bm = (int)(blockIdx.x / (unsigned)tiles_n);
+    const int m0 = bm * BM, n0 = (int)(blockIdx.x % (unsigned)tiles_n) * BB;
+    Rows ra;
+    Columns rb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        ra.row[i] = p.dY + (int64_t)min(m0 + (tid >> 3) + 32 * i, p.M - 1) * p.lddy;
+    floatx16 acc[2][2];
+    products<T>(
+        p.K, As, Bs, at,
+        [&](int k0) {
+            ra.load(k0, p.K, tid & 7);
+            rb.load(p.Wd, p.ldw, n0, p.N, k0, p.K, tid);
+        },
+        [&](int buf) {
+            ra.store(As[buf], tid);
+            rb.store(Bs[buf], tid);
+        },
+        acc);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int col = n0 + 64 * at.wn + 32 * j + at.c;
+        float sg = 0.0f, su = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t row = m0 + 64 * at.wm + 32 * i + acc_row(r, at.h);
+                if (row >= p.M || col >= p.N) continue;
+                const GradOut o = grad_at(p.act, acc[i][j][r], InFmt<T>::widen(p.G[row * p.ldg + col]),
+                                          InFmt<T>::widen(p.U[row * p.ldu + col]));
+                p.dG[row * p.lddg + col] = to_bits<T>(o.dg);
+                p.dU[row * p.lddu + col] = to_bits<T>(o.du);
+                if (p.H) p.H[row * p.ldh + col] = to_bits<T>(o.h);
+                sg += o.dg;
+                su += o.du;
+            }
+        if (p.parts) {
+            sg += __shfl_xor(sg, 32);
+            su += __shfl_xor(su, 32);
+            float* part = p.parts + 2 * (int64_t)(2 * bm + at.wm) * p.N;
+            if (at.h == 0 && col < p.N) {
+                part[col] = sg;
+                part[p.N + col] = su;
+            }
+        }
+    }
+}
+
+// Sums over the parts: 64 columns a workgroup, four lanes a column, each every
+// fourth part, joined in order.  Columns run over dG's and then dU's.
+__global__ __launch_bounds__(NT) void join_kernel(const float* parts, int64_t n_parts, int N,
+                                                  float* dbg, float* dbu) {
+    __shared__ float part[4][64];
+    const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int64_t col = (int64_t)blockIdx.x * 64 + c;
+    float sum = 0.0f;
+    if (col < 2 * (int64_t)N)
+        for (int64_t i = q; i < n_parts; i += 4) sum += parts[2 * i * N + col];
+    part[q][c] = sum;
+    __syncthreads();
+    if (q != 0 || col >= 2 * (int64_t)N) return;
+    sum = (part[0][c] + part[1][c]) + (part[2][c] + part[3][c]);
+    if (col < N) {
+        if (dbg) dbg[col] = sum;
+    } else if (dbu) {
+        dbu[col - N] = sum;
+    }
+}
+
+bool launchable(int64_t wgs) { return wgs < (int64_t(1) << 32) / NT; }
+
+}  // namespace
+
+template <In T>
+hipError_t launch_forward_regs(const Forward& p, hipStream_t s) {
+    const int64_t tiles_n = ((int64_t)p.N + BB / 2 - 1) / (BB / 2);
+    const int64_t wgs = tiles_n * (((int64_t)p.M + BM - 1) / BM);
+    if (!launchable(wgs)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(forward_regs_kernel<T>, dim3((unsigned)wgs), dim3(NT), 0, s, p,
+                       (int)tiles_n);
+    return hipGetLastError();
+}
+
+template <In T>
+hipError_t launch_grad_regs(const Grad& p, int64_t* parts, hipStream_t s) {
+    const int64_t tiles_n = ((int64_t)p.N + BB - 1) / BB;
+    const int64_t wgs = tiles_n * (((int64_t)p.M + BM - 1) / BM);
+    if (!launchable(wgs)) return hipErrorInvalidConfiguration;
+    *parts = parts_for(p.M, BM);
+    hipLaunchKernelGGL(grad_regs_kernel<T>, dim3((unsigned)wgs), dim3(NT), 0, s, p, (int)tiles_n);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(const float* parts, int64_t n_parts, int N, float* dbg, float* dbu,
+                       hipStream_t s) {
+    const int64_t wgs = (2 * (int64_t)N + 63) / 64;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)wgs), dim3(NT), 0, s, parts, n_parts, N, dbg,
+                       dbu);
+    return hipGetLastError();
+}
+
+template hipError_t launch_forward_regs<In::BF16>(const Forward&, hipStream_t);
+template hipError_t launch_forward_regs<In::F16>(const Forward&, hipStream_t);
+template hipError_t launch_grad_regs<In::BF16>(const Grad&, int64_t*, hipStream_t);
+template hipError_t launch_grad_regs<In::F16>(const Grad&, int64_t*, hipStream_t);
+
+template <In T>
+hipError_t launch_forward(const Forward& p, hipStream_t s) { return launch_forward_regs<T>(p, s); }
+template <In T>
+hipError_t launch_grad(const Grad& p, int64_t* parts, hipStream_t s) {
+    return launch_grad_regs<T>(p, parts, s);
+}
+template hipError_t launch_forward<In::BF16>(const Forward&, hipStream_t);
+template hipError_t launch_forward<In::F16>(const Forward&, hipStream_t);
+template hipError_t launch_grad<In::BF16>(const Grad&, int64_t*, hipStream_t);
+template hipError_t launch_grad<In::F16>(const Grad&, int64_t*, hipStream_t);
+
+}  // namespace gated
+}  // namespace dgt

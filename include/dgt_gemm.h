@@ -75,7 +75,7 @@ enum gemm_dtype { GEMM_DTYPE_F32 = 0, GEMM_DTYPE_BF16 = 1, GEMM_DTYPE_F16 = 2 };
 
 enum gemm_status {
     GEMM_OK = 0,
-    GEMM_ERR_DIM = -1,          /* M, N or K negative; MX4 and
+    GEMM_ERR_DIM = -1,          /* M, N or K negative; MX4, gated, W4 and
                                    orthogonalisation: past their limits      */
     GEMM_ERR_LD = -2,           /* lda < max(1,K), ldb < max(1,N) or
                                    ldc < max(1,N)                            */
@@ -88,19 +88,22 @@ enum gemm_status {
                                    support this shape / size                 */
     GEMM_ERR_LAUNCH = -6,       /* the HIP runtime rejected a kernel launch  */
     GEMM_ERR_ARG = -7,          /* dtype not a gemm_dtype, a transpose flag
-                                   other than 0 or 1, a negative batch,
+                                   other than 0 or 1, an activation or
+                                   group that is none, a negative batch,
                                    splits or workspace size, or a stride
                                    outside [0, 2^48)                         */
     GEMM_ERR_WORKSPACE = -8,    /* gemm_splitk, gemm_streamk,
-                                   gemm_orthogonalize: workspace NULL or
-                                   smaller than the call's workspace size    */
+                                   gemm_orthogonalize, gemm_gated_grad:
+                                   workspace NULL or smaller than the call's
+                                   workspace size                            */
     GEMM_ERR_SCRATCH = -9,      /* gemm_splitk_noalloc: the shape's partials
                                    (gemm_splitk_workspace_size) exceed
                                    DGT_GEMM_NOALLOC_SCRATCH_BYTES            */
-    GEMM_ERR_ALIGN = -10        /* MX4 codes or scales whose base or row
-                                   pitch is not a multiple of 16 bytes, or a
-                                   gemm_orthogonalize workspace whose base
-                                   is not                                    */
+    GEMM_ERR_ALIGN = -10        /* MX4 codes or scales, or W4 codes, whose
+                                   base or row pitch is not a multiple of 16
+                                   bytes, or a gemm_orthogonalize or
+                                   gemm_gated_grad workspace whose base is
+                                   not                                       */
 };
 
 /* Kernel ladder (for measurement and tests; GEMM_VARIANT_AUTO is what
@@ -433,6 +436,131 @@ int gemm_orthogonalize(int dtype, int M, int N, const void* G, int ldg,
 /* Bytes of workspace gemm_orthogonalize needs (0 for an empty call), or a
  * negative status for arguments outside its limits.  Host only. */
 int64_t gemm_orthogonalize_workspace_size(int M, int N, int batch);
+
+/* ------------------------------------------------- gated feed-forward block
+ *
+ * The first half of a gated feed-forward block, both projections, the
+ * activation and the elementwise product in one kernel:
+ *
+ *     g = X*Wg^T + bias_g,   u = X*Wu^T + bias_u,   H = act(g) * u
+ *
+ * X is M x K, Wg and Wu are N x K (a linear layer's weights as stored), H is
+ * M x N; X, the weights and H are raw 16-bit values of one format, `dtype`
+ * (GEMM_DTYPE_BF16 or GEMM_DTYPE_F16).  The biases are fp32, N values, each
+ * optional (NULL).  Sums are fp32; H, and g and u where they are asked for (G and U,
+ * each optional: what the gradient needs), are each rounded once, to nearest
+ * even, H from the unrounded g and u.  The two weights may be row halves, and G and U
+ * column halves, of one matrix.  K == 0 leaves the biases (or zeros).
+ *
+ * Activations: */
+enum gemm_activation {
+    GEMM_ACT_SILU = 0,          /* x / (1 + exp(-x))                         */
+    GEMM_ACT_GELU = 1,          /* x * P(normal variable < x)                */
+    GEMM_ACT_GELU_TANH = 2,     /* x/2 * (1 + tanh(sqrt(2/pi) *
+                                   (x + 0.044715*x^3)))                      */
+    GEMM_ACT_RELU = 3,          /* max(x, 0); slope 0 at 0                   */
+    GEMM_ACT_SIGMOID = 4,       /* 1 / (1 + exp(-x))                         */
+    GEMM_ACT_IDENTITY = 5       /* x                                         */
+};
+
+/* Largest M, N and K of the gated calls and of those on 4-bit weights with
+ * group scales (N: half of it for gemm_w4_gated; GEMM_ERR_DIM above). */
+#define DGT_GEMM_GATED_MAX_DIM (1 << 28)
+
+/* Any alignment of 2 bytes.  Rows on 16-byte boundaries (bases and pitches of X
+ * and the weights) with pitches below 2^24 take the faster kernels.  H, G
+ * and U must not overlap each other or an input (GEMM_ERR_OVERLAP; column
+ * ranges of one matrix, with one pitch, do not overlap).  Checks run in this order:
+ * dtype and activation, dimensions, pitches, quick return for an empty H, null
+ * pointers, overlap. */
+int gemm_gated(int dtype, int act, int M, int N, int K, const uint16_t* X, int ldx,
+               const uint16_t* Wg, int ldwg, const uint16_t* Wu, int ldwu,
+               const float* bias_g, const float* bias_u, uint16_t* H, int ldh,
+               uint16_t* G, int ldg, uint16_t* U, int ldu, void* stream);
+
+/* The gradient at the projections of a block whose second half is Y = H*Wd^T,
+ * from dY (M x K) and Wd as stored (K x N):
+ *
+ *     dh = dY*Wd,  dG = dh * U * act'(G),  dU = dh * act(G)
+ *
+ * with G and U as gemm_gated kept them; H = act(G) * U again where it is asked
+ * for (optional; what Wd's gradient dY^T*H needs), and the biases' gradients, the column sums of dG
+ * and dU before their rounding (each optional, N floats).  dh itself never
+ * reaches memory.  With dG and dU column halves of one matrix D and the weights row halves of
+ * one matrix W, the rest of the block's gradient is two products: dX = D*W,
+ * dW = D^T*X.  dG may be G's memory and dU may be U's (same base and pitch);
+ * otherwise no output may overlap another or an input.
+ *
+ * Only calls that ask for a bias's gradient need the workspace (16-byte aligned,
+ * gemm_gated_grad_workspace_size bytes; GEMM_ERR_WORKSPACE, GEMM_ERR_ALIGN); it must
+ * stay untouched until the work on `stream` has finished, and calls that may run at
+ * the same time need workspaces of their own.  The sums' order is fixed.  M == 0
+ * writes zeros to them.  Checks as for gemm_gated. */
+int gemm_gated_grad(int dtype, int act, int M, int N, int K, const uint16_t* dY,
+                    int lddy, const uint16_t* Wd, int ldw, const uint16_t* G, int ldg,
+                    const uint16_t* U, int ldu, uint16_t* dG, int lddg, uint16_t* dU,
+                    int lddu, uint16_t* H, int ldh, float* dbias_g, float* dbias_u,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a gemm_gated_grad call with a bias's gradient needs, or a
+ * negative status.  Host only. */
+int64_t gemm_gated_grad_workspace_size(int M, int N);
+
+/* ------------------------------------- 4-bit weights with group scales (W4)
+ *
+ * A row of K elements is cut into groups of `group` (32, 64 or 128)
+ * consecutive k; element k stands for
+ *
+ *     s * (q - z)
+ *
+ * with q its code 0 .. 15, s the group's scale and z its zero point.  Storage
+ * of an operand of M rows:
+ *     codes   as MX4's: row i at Q + i*ldq, k in the low (k even) or high (k
+ *             odd) half of byte k/2; ldq >= gemm_mx4_code_pitch(K), at most
+ *             DGT_GEMM_MX4_MAX_PITCH, and Q and ldq multiples of 16 bytes
+ *             (GEMM_ERR_ALIGN).  What the last 16 bytes hold past K is never used.
+ *     scales  row i at S + i*lds (16-bit elements of `scale_dtype`,
+ *             GEMM_DTYPE_BF16 or GEMM_DTYPE_F16), lds >= ceil(K/group)
+ *     zeros   row i at Z + i*ldz, one byte per group, 0 .. 255; Z == NULL: 8
+ *             everywhere (ldz is not looked at)
+ *
+ * Checks run in this order: dtypes, activation and group, dimensions, pitches,
+ * quick return for an empty result, null pointers, alignment, overlap. */
+
+/* Q, S, Z <- the M x K matrix X in the input format `dtype`, any alignment.
+ * Per group, over its elements and 0: with Z, s = (max - min)/15 and
+ * z = -min/s to the nearest whole number; with Z == NULL, s = max(max/7, -min/8).
+ * s is rounded to fp32 and then to its type (past the type's largest value: that
+ * value); x becomes the whole number nearest to x/s (ties to even) plus z, within
+ * 0 .. 15.  A group whose scale comes out as 0 gets the code z.  A
+ * group that holds an infinity or a NaN gets the scale NaN and zero codes.  The codes past K in the
+ * last 16 bytes are written as zeros; nothing past those is written. */
+int gemm_w4_quantize(int dtype, int group, int scale_dtype, int M, int K,
+                     const void* X, int ldx, uint8_t* Q, int ldq, void* S, int lds,
+                     uint8_t* Z, int ldz, void* stream);
+
+/* Y (M x K, row pitch ldy elements, format `dtype`) <- the operand's values,
+ * exact in FP32, rounded to nearest even otherwise. */
+int gemm_w4_dequantize(int dtype, int group, int scale_dtype, int M, int K,
+                       const uint8_t* Q, int ldq, const void* S, int lds,
+                       const uint8_t* Z, int ldz, void* Y, int ldy, void* stream);
+
+/* C <- alpha*A*W^T + beta*C + bias with 16-bit A (`dtype`, M x K, any alignment)
+ * and W the N x K operand Q, S, Z: for products of few rows.  Weights are not rounded:
+ * within a group x*q and x are summed apart in fp32, and s*(sum xq - z*sum x) is
+ * added up in fp32.  bias: NULL or N floats.  alpha == 0 or K == 0 reads neither
+ * operand, beta == 0 does not read C. */
+int gemm_w4_a16(int dtype, int group, int scale_dtype, int M, int N, int K,
+                float alpha, const uint16_t* A, int lda, const uint8_t* Q, int ldq,
+                const void* S, int lds, const uint8_t* Z, int ldz, float beta,
+                float* C, int ldc, const float* bias, void* stream);
+
+/* gemm_gated on such weights, one operand of 2N rows: Wg's, then Wu's.  H as
+ * there, M x N; no pre-activations are kept. */
+int gemm_w4_gated(int dtype, int act, int group, int scale_dtype, int M, int N, int K,
+                  const uint16_t* X, int ldx, const uint8_t* Q, int ldq, const void* S,
+                  int lds, const uint8_t* Z, int ldz, const float* bias_g,
+                  const float* bias_u, uint16_t* H, int ldh, void* stream);
 
 /* The rung GEMM_VARIANT_AUTO picks for this call (dtype: enum gemm_dtype;
  * trans_a, trans_b as for gemm_ex), or a negative status if the arguments
