@@ -58,7 +58,31 @@ __device__ __forceinline__ Logistic logistic(float x) {
 
 constexpr float kTanhA = 1.59576912f;              // 2 * sqrt(2/pi)
 constexpr float kTanhB = 0.044715f;
-constexpr float kInvSqrt2 = 0.70710678f, kInvSqrt2Pi = 0.39894228f;
+constexpr float kInvSqrt2Pi = 0.39894228f;
+
+// P(normal variable < x) and exp(-x^2/2).  The tail below -|x| is exp(-x^2/2) times t
+// times a polynomial in t = 1/(1 + 0.4|x|): a least-maximum fit of
+// erfcx(|x|/sqrt 2)/(2t) over 0 < t <= 1 in 64 bits, its relative error 1.3e-7, and 3.6e-7 as
+// evaluated here.  (A tail as 1 - P(x < |x|) would lose its digits.)
+struct Normal {
+    float below, bell;
+};
+__device__ __forceinline__ Normal normal(float x) {
+    const float bell = __builtin_exp2f(-0.72134752f * (x * x));
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.4f, fabsf(x), 1.0f));
+    float q = 0.046239819f;
+    q = fmaf(q, t, -0.26906604f);
+    q = fmaf(q, t, 0.59885973f);
+    q = fmaf(q, t, -0.56983966f);
+    q = fmaf(q, t, 0.12439930f);
+    q = fmaf(q, t, -0.0086596236f);
+    q = fmaf(q, t, 0.17206378f);
+    q = fmaf(q, t, 0.26768470f);
+    q = fmaf(q, t, 0.31916407f);
+    q = fmaf(q, t, 0.31915379f);
+    const float tail = 0.5f * bell * t * q;
+    return Normal{x < 0.0f ? tail : 1.0f - tail, bell};
+}
 
 // act(x), and with kSlope its derivative.  A NaN stays one.
 template <bool kSlope>
@@ -70,10 +94,9 @@ __device__ __forceinline__ float act_at(Act act, float x, float& slope) {
             return x * s.pos;
         }
         case Act::Gelu: {
-            // the complement keeps the lower tail's digits
-            const float p = 0.5f * erfcf(-kInvSqrt2 * x);
-            if (kSlope) slope = fmaf(x * kInvSqrt2Pi, expf(-0.5f * x * x), p);
-            return x * p;
+            const Normal n = normal(x);
+            if (kSlope) slope = fmaf(x * kInvSqrt2Pi, n.bell, n.below);
+            return x * n.below;
         }
         case Act::GeluTanh: {  // 0.5 * x * (1 + tanh(y/2)) = x * logistic(y)
             const float x2 = x * x;

@@ -17,6 +17,10 @@
 
 #include <type_traits>
 
+// For the kernels whose bodies are lambdas over register arrays: one that is
+// not inlined puts those arrays into scratch memory.
+#define DGT_INLINE __attribute__((always_inline))
+
 namespace dgt {
 
 struct GemmParams {

@@ -304,16 +304,5 @@ template hipError_t launch_forward_regs<In::F16>(const Forward&, hipStream_t);
 template hipError_t launch_grad_regs<In::BF16>(const Grad&, int64_t*, hipStream_t);
 template hipError_t launch_grad_regs<In::F16>(const Grad&, int64_t*, hipStream_t);
 
-template <In T>
-hipError_t launch_forward(const Forward& p, hipStream_t s) { return launch_forward_regs<T>(p, s); }
-template <In T>
-hipError_t launch_grad(const Grad& p, int64_t* parts, hipStream_t s) {
-    return launch_grad_regs<T>(p, parts, s);
-}
-template hipError_t launch_forward<In::BF16>(const Forward&, hipStream_t);
-template hipError_t launch_forward<In::F16>(const Forward&, hipStream_t);
-template hipError_t launch_grad<In::BF16>(const Grad&, int64_t*, hipStream_t);
-template hipError_t launch_grad<In::F16>(const Grad&, int64_t*, hipStream_t);
-
 }  // namespace gated
 }  // namespace dgt

@@ -102,7 +102,9 @@ __global__ __launch_bounds__(NT) void quantize_kernel(const void* Xv, int64_t ld
                 finite = __shfl_xor((int)finite, d) && finite;
             }
             const double hi = top, lo = -(double)low;
-            const float wide = (float)(Z ? (hi + lo) / 15.0 : fmax(hi / 7.0, lo / 8.0));
+            float wide = (float)(Z ? (hi + lo) / 15.0 : fmax(hi / 7.0, lo / 8.0));
+            // two roundings, as documented: the compiler would join them into one
+            asm("" : "+v"(wide));
             uint16_t bits = s_bf16 ? gated::to_bits<In::BF16>(wide) : gated::to_bits<In::F16>(wide);
             const uint16_t inf = s_bf16 ? 0x7f80 : 0x7c00;
             if (bits == inf) bits = inf - 1;

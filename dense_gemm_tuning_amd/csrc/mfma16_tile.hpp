@@ -209,9 +209,74 @@ struct MnOperand {
 // raw (R x R, row pitch R, every element written; a stream-K partial tile).
 struct BlasEpilogue {};
 
-template <In T, int R, bool TA, bool TB, bool kEdge, bool kTail, typename Epi = BlasEpilogue>
+// Accumulators reach memory through the wavefront's LDS region, one row of
+// MFMA tiles (32 x R/2 fp32) at a time, so that a lane handles 8 neighbouring
+// columns (or, mirrored, 8 neighbouring rows) with 16-byte accesses.  Column c of
+// row r sits at c ^ 32*(r/4 & 1): the two half-waves of an accumulator write rows 4
+// apart, which then differ in banks.
+
+template <int R>
+struct Chunk {
+    static constexpr int W = R / 2;           // columns
+    static constexpr int GROUPS = W / 8;      // column groups of 8
+    float* mem;
+    __device__ static int at(int r, int c) { return r * W + (c ^ (32 * ((r >> 2) & 1))); }
+    // Lanes read what other lanes of the wavefront wrote: LDS keeps their
+    // order, the compiler has to as well.
+    __device__ static void fence() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    // MFMA tiles of tile row ti.
+    __device__ void put(const floatx16 (&acc)[Geo<R>::TM], int lane) const {
+        const int h = lane >> 5;
+        fence();
+#pragma unroll
+        for (int tj = 0; tj < Geo<R>::TM; ++tj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                mem[at(8 * (r >> 2) + 4 * h + (r & 3), tj * 32 + (lane & 31))] = acc[tj][r];
+        fence();
+    }
+    __device__ void row8(int r, int c, float (&v)[8]) const {
+        const floatx4 a = *reinterpret_cast<const floatx4*>(mem + at(r, c));
+        const floatx4 b = *reinterpret_cast<const floatx4*>(mem + at(r, c + 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    }
+    __device__ void col8(int r, int c, float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = mem[at(r + e, c)];
+    }
+    void __device__ set_row8(int r, int c, const float (&v)[8]) const {
+        *reinterpret_cast<floatx4*>(mem + at(r, c)) = floatx4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<floatx4*>(mem + at(r, c + 4)) = floatx4{v[4], v[5], v[6], v[7]};
+    }
+    // The lane's pieces of a chunk: piece i is 8 columns of a row, or
+    // (mirrored) 8 rows of a column.
+    static constexpr int PIECES = 32 * W / 8 / 64;
+    __device__ static int row(int i, int lane) { return (64 * i + lane) / GROUPS; }
+    __device__ static int col(int i, int lane) { return (64 * i + lane) % GROUPS * 8; }
+    __device__ static int mirror_col(int i, int lane) { return (64 * i + lane) % W; }
+    __device__ static int mirror_row(int i, int lane) { return (64 * i + lane) / W * 8; }
+};
+
+// Where an operand B stored N x K comes from.  OneB: the call's.  TwoB: two such
+// operands, the columns of the second beside those of the first: n0 and p.N then count
+// columns of either, a tile covers R/2 of them, and of a wavefront's R/2 staged
+// rows the first half are p.B's rows and the second half B2's same rows.
+struct OneB {};
+struct TwoB {
+    const void* B2;
+    int64_t ldb2;
+};
+
+
+template <In T, int R, bool TA, bool TB, bool kEdge, bool kTail, typename Epi = BlasEpilogue,
+          typename SrcB = OneB>
 __device__ __forceinline__ void dma_tile(const GemmParams& p, int m0, int n0, float* raw,
-                                         const Epi& epi = {}) {
+                                         const Epi& epi = {}, const SrcB& src = {}) {
     constexpr bool AK = !TA, BKc = TB;
     constexpr int TM = Geo<R>::TM;
     using OpA = typename std::conditional<AK, KcOperand<R>, MnOperand<R>>::type;
@@ -239,8 +304,19 @@ __device__ __forceinline__ void dma_tile(const GemmParams& p, int m0, int n0, fl
     OpB opb;
     opa.template init<kEdge>(static_cast<const uint16_t*>(p.A), p.lda, m0, wm, wave, lane, nk,
                              p.M, p.K);
-    opb.template init<kEdge>(static_cast<const uint16_t*>(p.B), p.ldb, n0, wn, wave, lane, nk,
-                             p.N, p.K);
+    if constexpr (std::is_same<SrcB, TwoB>::value) {
+        static_assert(BKc, "two operands B are stored N x K");
+        // wavefront w copies R/4 staged rows: of the first operand (w even) or
+        // the second, from row n0 + R/4 * (w/2) on
+        const bool second = wave & 1;
+        opb.template init<kEdge>(static_cast<const uint16_t*>(second ? src.B2 : p.B),
+                                 second ? src.ldb2 : p.ldb,
+                                 n0 + Geo<R>::KC_ROWS * ((wave >> 1) - wave), wn, wave, lane, nk,
+                                 p.N, p.K);
+    } else {
+        opb.template init<kEdge>(static_cast<const uint16_t*>(p.B), p.ldb, n0, wn, wave, lane, nk,
+                                 p.N, p.K);
+    }
 
     floatx16 acc[TM][TM];
 #pragma unroll

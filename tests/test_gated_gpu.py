@@ -78,6 +78,39 @@ def test_forward_is_exact_on_whole_numbers(M, N, K, dtype):
             assert torch.equal(U.cpu(), u.to(DT[dtype])) and u_ok()
 
 
+# sizes whose tiles are the largest: whole ones, cut ones, and K ending inside a slice group
+LARGE = [(2304, 2432, 128), (2100, 2100, 128), (2100, 2101, 200), (2900, 3336, 256)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_tiles_are_exact_on_whole_numbers(M, N, K, dtype):
+    gen = gen_for(M, N, K, 13)
+    X, W = ints(gen, M, K, top=2).to(DT[dtype]).cuda(), ints(gen, 2 * N, K, top=2).to(DT[dtype]).cuda()
+    b = ints(gen, 2, N).cuda()
+    want = (X.float() @ W.float().T) + b.flatten()  # whole numbers below 2^24: exact in fp32
+    H = torch.empty(M, N, dtype=DT[dtype], device="cuda")
+    P = torch.empty(M, 2 * N, dtype=DT[dtype], device="cuda")
+    dgt.check(dgt.gated(X, W[:N], W[N:], H, act="relu", bias_g=b[0], bias_u=b[1], G=P[:, :N], U=P[:, N:]))
+    assert torch.equal(P, want.to(DT[dtype]))
+    assert torch.equal(H, (want[:, :N].clamp(min=0) * want[:, N:]).to(DT[dtype]))
+    dgt.check(dgt.gated(X, W[:N], W[N:], H, act="identity"))
+    assert torch.equal(H, ((want - b.flatten())[:, :N] * (want - b.flatten())[:, N:]).to(DT[dtype]))
+    # the gradient of the same size: Wd is K x N
+    dY, Wd = ints(gen, M, K, top=1).to(DT[dtype]).cuda(), ints(gen, K, N + 8 - N % 8, top=1).to(DT[dtype]).cuda()[:, :N]
+    G, U = ints(gen, M, N).to(DT[dtype]).cuda(), ints(gen, M, N).to(DT[dtype]).cuda()
+    D = torch.full((M, 2 * N + 8), 77.0, dtype=DT[dtype], device="cuda")
+    sums = torch.empty(2, N, device="cuda")
+    dgt.check(dgt.gated_grad(dY, Wd, G, U, D[:, :N], D[:, N:2 * N], act="relu", H=H, dbias_g=sums[0], dbias_u=sums[1]))
+    dh, g, u = dY.float() @ Wd.float(), G.float(), U.float()
+    dg, du = dh * u * (g > 0), dh * g.clamp(min=0)
+    assert torch.equal(D[:, :N], dg.to(DT[dtype])) and torch.equal(D[:, N:2 * N], du.to(DT[dtype]))
+    assert torch.equal(H, (g.clamp(min=0) * u).to(DT[dtype])) and (D[:, 2 * N:] == 77.0).all()
+    assert torch.equal(sums.double(), torch.stack([dg.double().sum(0), du.double().sum(0)]))
+    dgt.check(dgt.gated_grad(dY, Wd, G, U, D[:, :N], D[:, N:2 * N], act="identity"))
+    assert torch.equal(D[:, :N], (dh * u).to(DT[dtype])) and torch.equal(D[:, N:2 * N], (dh * g).to(DT[dtype]))
+
+
 def close_forward(H, G, U, X, Wg, Wu, bg, bu, act, dtype, what):
     h, g, u, eg, eu = gp.forward(X, Wg, Wu, bg, bu, act)
     t = DT[dtype]

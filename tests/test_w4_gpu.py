@@ -77,6 +77,20 @@ def test_packing_matches_the_definition(rows, K, dtype, zeros):
                 assert (Yw[:, K:] == 5.0).all()
 
 
+@pytest.mark.parametrize("st,m", [("f16", 1 + 2.0 ** -11), ("bf16", 1 + 2.0 ** -8)])
+def test_scales_are_rounded_twice(st, m):
+    """(15 m + 2^-24)/15 lies above m, half way between two scales, by less than fp32 shows: fp32's
+    rounding gives m and the tie the even side, 1; a single rounding would go up."""
+    x = torch.zeros(3, 32)
+    x[0, 3], x[0, 30] = 15 * m, -2.0 ** -24
+    x[1] = 2 * x[0]
+    Q, S, Z = dgt.w4_empty(3, 32, group=32, scale_dtype=DT[st])
+    dgt.check(dgt.quantize_w4(x.cuda(), Q, S, Z, group=32))
+    q, s, z = gp.quantize(x.double().numpy(), 32, DT[st], True)
+    assert s[:, 0].tolist() == [1.0, 2.0, 0.0] and torch.equal(S.cpu(), s)
+    assert torch.equal(Q.cpu(), gp.pack(q)) and np.array_equal(Z.cpu().numpy(), z)
+
+
 @pytest.mark.parametrize("st", ["bf16", "f16"])
 @pytest.mark.parametrize("zeros", [True, False])
 def test_unusual_groups(zeros, st):
