@@ -153,6 +153,8 @@ template <In T> hipError_t launch_grad_regs(const Grad& p, int64_t* parts, hipSt
 // out[n] <- the sums over `parts` parts (either pointer may be null).
 hipError_t launch_join(const float* parts, int64_t n_parts, int N, float* dbg, float* dbu,
                        hipStream_t s);
+bool strip_eligible(const Forward& p);
+template <In T> hipError_t launch_forward_strip(const Forward& p, hipStream_t s);
 template <In T> hipError_t launch_forward(const Forward& p, hipStream_t s);
 template <In T> hipError_t launch_grad(const Grad& p, int64_t* parts, hipStream_t s);
 

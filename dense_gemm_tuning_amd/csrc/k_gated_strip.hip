@@ -1,0 +1,49 @@
+// k_gated_strip.hip -- which strips (strip.hpp) the gated projections of up to
+// 64 rows take with 16-bit weights.
+#include "strip.hpp"
+
+namespace dgt {
+namespace gated {
+
+namespace {
+
+// RB blocks of 16 rows, NG groups of GR stored rows of ROWB bytes a step.
+template <int RB, int NG, int GR, int ROWB>
+using Cfg = strip::Cfg<false, 0, true, RB, NG, GR, ROWB>;
+
+}  // namespace
+
+// 16-byte aligned rows of whole 16-byte pieces (a piece is then inside K or
+// outside), and offsets of a group's rows below 2^31.
+bool strip_eligible(const Forward& p) {
+    auto rows_ok = [](const void* at, int64_t ld) {
+        return rows_16b_aligned(at, ld, 2) && ld < kMaxBufferPitch;
+    };
+    return p.M <= kSkinnyMaxM && p.K > 0 && p.K % 8 == 0 && rows_ok(p.X, p.ldx) &&
+           rows_ok(p.Wg, p.ldwg) && rows_ok(p.Wu, p.ldwu);
+}
+
+template <In T>
+hipError_t launch_forward_strip(const Forward& p, hipStream_t s) {
+    strip::Params q = {};
+    q.M = p.M; q.N = p.N; q.K = p.K;
+    q.X = p.X; q.ldx = p.ldx;
+    q.W[0] = reinterpret_cast<const uint8_t*>(p.Wg); q.ldw[0] = 2 * p.ldwg;
+    q.W[1] = reinterpret_cast<const uint8_t*>(p.Wu); q.ldw[1] = 2 * p.ldwu;
+    q.chunks = p.K / 8;
+    q.act = p.act;
+    q.bg = p.bg; q.bu = p.bu;
+    q.H = p.H; q.ldh = p.ldh;
+    q.G = p.G; q.ldg = p.ldg;
+    q.U = p.U; q.ldu = p.ldu;
+    if (p.M > 32) return strip::launch<T, Cfg<4, 4, 32, 128>>(q, s);
+    if (p.M > 16) return strip::launch<T, Cfg<2, 8, 16, 256>>(q, s);
+    if (p.N <= 16 * dma::kCUs) return strip::launch<T, Cfg<1, 2, 16, 256>>(q, s);
+    if (p.N <= 32 * dma::kCUs) return strip::launch<T, Cfg<1, 4, 16, 256>>(q, s);
+    return strip::launch<T, Cfg<1, 8, 16, 256>>(q, s);
+}
+template hipError_t launch_forward_strip<In::BF16>(const Forward&, hipStream_t);
+template hipError_t launch_forward_strip<In::F16>(const Forward&, hipStream_t);
+
+}  // namespace gated
+}  // namespace dgt

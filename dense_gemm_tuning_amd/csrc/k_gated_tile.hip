@@ -282,6 +282,7 @@ hipError_t grad_tiles(const Grad& p, int64_t* parts, hipStream_t s) {
 
 template <In T>
 hipError_t launch_forward(const Forward& p, hipStream_t s) {
+    if (strip_eligible(p)) return launch_forward_strip<T>(p, s);
     if (p.K == 0 || !rows_ok(p.X, p.ldx) || !rows_ok(p.Wg, p.ldwg) || !rows_ok(p.Wu, p.ldwu))
         return launch_forward_regs<T>(p, s);
     return take_128(p.M, 2 * (int64_t)p.N) ? forward_tiles<T, 128>(p, s) : forward_tiles<T, 256>(p, s);

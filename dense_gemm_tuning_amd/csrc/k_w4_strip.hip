@@ -1,0 +1,69 @@
+// k_w4_strip.hip -- which strips (strip.hpp) a product of few rows with 4-bit
+// weights takes.
+#include "strip.hpp"
+
+namespace dgt {
+namespace w4 {
+
+namespace {
+
+using strip::Cfg;
+
+// 2^LG blocks of 32 k a scale group.
+template <In T, int LG, bool kGated>
+hipError_t launch_group(const strip::Params& p, hipStream_t s) {
+    constexpr int kPair = kGated ? 2 : 1;
+    if (p.M > 16) return strip::launch<T, Cfg<true, LG, kGated, 2, 4, 16, 128>>(p, s);
+    if (p.N <= 16 * dma::kCUs) return strip::launch<T, Cfg<true, LG, kGated, 1, kPair, 16, 128>>(p, s);
+    return strip::launch<T, Cfg<true, LG, kGated, 1, LG == 2 ? 4 : 2, 32, 128>>(p, s);
+}
+
+template <bool kGated>
+hipError_t launch_strips(In t, int log_group, const strip::Params& p, hipStream_t s) {
+    auto go = [&](auto tc) {
+        constexpr In T = decltype(tc)::value;
+        return log_group == 5   ? launch_group<T, 0, kGated>(p, s)
+               : log_group == 6 ? launch_group<T, 1, kGated>(p, s)
+                                : launch_group<T, 2, kGated>(p, s);
+    };
+    return t == In::BF16 ? go(std::integral_constant<In, In::BF16>{})
+                         : go(std::integral_constant<In, In::F16>{});
+}
+
+strip::Params of_weight(const Weight& w, int M, int N, int K, const uint16_t* X, int64_t ldx) {
+    strip::Params p = {};
+    p.M = M; p.N = N; p.K = K;
+    p.X = X; p.ldx = ldx;
+    p.chunks = mx4::blocks(K);
+    p.groups = groups(K, w.log_group);
+    p.lds = w.lds; p.ldz = w.ldz;
+    p.s_bf16 = w.s_bf16;
+    for (int m = 0; m < 2; ++m) {  // the second half's rows start at row N
+        p.W[m] = w.Q + (int64_t)m * N * w.ldq;
+        p.ldw[m] = w.ldq;
+        p.S[m] = w.S + (int64_t)m * N * w.lds;
+        p.Z[m] = w.Z ? w.Z + (int64_t)m * N * w.ldz : nullptr;
+    }
+    return p;
+}
+
+}  // namespace
+
+hipError_t launch_product(In t, const Product& p, hipStream_t s) {
+    strip::Params q = of_weight(p.w, p.M, p.N, p.K, p.A, p.lda);
+    q.alpha = p.alpha; q.beta = p.beta;
+    q.C = p.C; q.ldc = p.ldc;
+    q.bias = p.bias;
+    return launch_strips<false>(t, p.w.log_group, q, s);
+}
+
+hipError_t launch_gated(In t, const Gated& p, hipStream_t s) {
+    strip::Params q = of_weight(p.w, p.M, p.N, p.K, p.X, p.ldx);
+    q.act = p.act;
+    q.bg = p.bg; q.bu = p.bu;
+    q.H = p.H; q.ldh = p.ldh;
+    return launch_strips<true>(t, p.w.log_group, q, s);
+}
+
+}  // namespace w4
+}  // namespace dgt

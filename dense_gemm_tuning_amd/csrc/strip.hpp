@@ -1,0 +1,605 @@
+// strip.hpp -- products of few rows with weights stored N x K (16-bit, or 4-bit
+// with group scales), plain or gated: the kernel of k_gated_strip.hip and
+// k_w4_strip.hip.  The time is the time to stream the weights once.
+//
+// A workgroup owns a strip of outputs over the whole of K, each of its 8
+// waves one range of it; the partial tiles are summed in LDS in wave order
+// (deterministic, no atomics, no workspace).  A wave copies its pieces of the
+// weights straight into a private LDS ring by buffer loads that write LDS, so
+// the loop has no workgroup barrier: a step is ROWB bytes of every stored row of the
+// strip, in NG groups of GR rows, copied D = NS - 1 groups ahead.  Of a gated
+// strip's groups the even ones are the gate's rows and the odd ones the other
+// projection's rows for the same outputs.
+//
+// Lane (i, g) = (lane % 16, lane / 16) of a 16-row block takes 8 of every 32 k of row
+// i: 16 bytes of a 16-bit weight (k 8g .. 8g+7), a dword of codes.  Of a scale
+// group of GB blocks of 32 k it takes k 8*GB*g .. 8*GB*(g+1)-1, GB neighbouring dwords, as GB
+// products.  The activations are loaded the same way into registers a step ahead.
+// Chunk c (16 bytes) of row r sits at c ^ swz(r) in LDS: 16 rows reading one
+// chunk touch 16 distinct 16-byte bank groups.
+//
+// 4-bit weights: a code in a byte, read as an E4M3 number, is the code times
+// 2^-9 (they are that format's subnormal numbers and its first binade), so the scaled
+// conversion gives the codes themselves, exactly, two per instruction; no
+// weight is rounded.  The even codes of a dword come from its low halves of bytes and the
+// odd ones from the high halves, so the activations are put into the order 0 2 4 6 1 3
+// 5 7 once a step.  Per group the products sum x*q, and sum x (a product with ones, once
+// for all rows of the strip), are joined as acc += s * (sum xq - z * sum x).
+#pragma once
+
+#include "dma_common.hpp"
+#include "mx4_device.hpp"
+#include "skinny_common.hpp"
+#include "w4.hpp"
+
+namespace dgt {
+namespace strip {
+
+using mx4::static_for;
+using skinny::u32x4_any;
+
+constexpr int NW = 8;        // waves per workgroup
+constexpr int kBPolicy = 2;  // cache policy of the weights' copies: nt (streamed once)
+
+struct Params {
+    int M, N, K;
+    const uint16_t* X;
+    int64_t ldx;                   // elements
+    const uint8_t* W[2];           // rows of output 0 on (plain: the first only)
+    int64_t ldw[2];                // bytes
+    int chunks;                    // 16-byte pieces of a row
+    const uint16_t* S[2];          // 4-bit weights: scales and zero points
+    const uint8_t* Z[2];           // (null: 8)
+    int64_t lds, ldz;
+    int groups;
+    bool s_bf16;
+    // gated
+    gated::Act act;
+    const float *bg, *bu;
+    uint16_t *H, *G, *U;
+    int64_t ldh, ldg, ldu;
+    // plain
+    float alpha, beta;
+    float* C;
+    int64_t ldc;
+    const float* bias;
+};
+
+// kW4: 4-bit weights, 2^LG blocks of 32 k a scale group.
+template <bool kW4_, int LG_, bool kGated_, int RB_, int NG_, int GR_, int ROWB_>
+struct Cfg {
+    static constexpr bool kW4 = kW4_, kGated = kGated_;
+    static constexpr int RB = RB_, NG = NG_, GR = GR_, ROWB = ROWB_;
+    static constexpr int NS = 4, D = NS - 1;
+    static constexpr int KS = kW4 ? 2 * ROWB : ROWB / 2;  // k per step
+    static constexpr int P = KS / 32;                     // 32-k blocks per step
+    static constexpr int CPS = ROWB / 16;                 // chunks of a row per step
+    static constexpr int NBK = GR / 16;                   // 16-row blocks per group
+    static constexpr int CB = NG * NBK;                   // ... per strip
+    static constexpr int ROWS = NG * GR;                  // stored rows per strip
+    static constexpr int COLS = kGated ? ROWS / 2 : ROWS; // outputs per strip
+    static constexpr int STAGE = GR * ROWB;
+    static constexpr int INSTR = STAGE / 1024, RPI = 1024 / ROWB, LPR = ROWB / 16;
+    static constexpr int GB = 1 << LG_;                   // blocks per scale group
+    static constexpr int GPS = kW4 ? P / GB : 1;          // scale groups per step
+    // Scales and zero points: a lane loads a step's of one stored row (GPS
+    // 16-bit values and GPS bytes), a step ahead.
+    static constexpr int NSC = kW4 ? (ROWS + 63) / 64 : 0;
+    static constexpr int SW = (GPS + 1) / 2, ZW = (GPS + 3) / 4;  // in dwords
+    static constexpr int LA = RB * P + 2 * NSC;  // vector loads per step besides the copies
+    // Whether the activations' sums per scale group are kept for the step, or
+    // made again for every group of rows (their registers are many when the scale groups are).
+    static constexpr bool kKeepSums = RB * GPS <= 4;
+    // rows of a reduction pass in one stage of all waves
+    static constexpr int RR = STAGE / (ROWS * 4) < 16 ? STAGE / (ROWS * 4) : 16;
+    static_assert(ROWB == 256 || ROWB == 128, "a row piece is 256 or 128 bytes");
+    static_assert(NG == 1 || NG == 2 || NG == 4 || NG == 8, "groups map onto the ring");
+    static_assert(!kGated || NG % 2 == 0, "a gated strip's groups come in pairs");
+    static_assert(!kW4 || P % GB == 0, "a scale group does not cross steps");
+    static_assert(RR >= 4, "a pass holds an accumulator's rows");
+    __device__ static int swz(int r) { return ROWB == 256 ? (r & 15) : ((r >> 1) & 7); }
+    // Loads of operands (one in each phase 0) from the phase that copied group cp of the
+    // wave's step t, D phases before, to that group's: in the first kFirst steps
+    // some of those phases are the prologue, which loads before it copies.
+    static constexpr int kFirst = NG >= D + 1 ? 0 : (D + NG - 1) / NG;
+    static constexpr int loads(int cp, int t) {
+        int n = 0;
+        for (int x = cp - D < -t * NG ? -t * NG : cp - D; x <= cp; ++x) n += x % NG == 0;
+        return n;
+    }
+};
+static_assert(Cfg<true, 2, false, 1, 4, 32, 128>::kFirst == 0 &&
+                  Cfg<true, 2, false, 1, 4, 32, 128>::loads(0, 0) == 1 &&
+                  Cfg<true, 2, false, 1, 4, 32, 128>::loads(3, 0) == 1 &&
+                  Cfg<true, 2, false, 1, 2, 32, 128>::loads(1, 0) == 1 &&
+                  Cfg<true, 2, false, 1, 2, 32, 128>::loads(0, 2) == 2 &&
+                  Cfg<true, 2, false, 1, 1, 16, 128>::kFirst == 3 &&
+                  Cfg<true, 2, false, 1, 1, 16, 128>::loads(0, 3) == 4 &&
+                  Cfg<false, 0, true, 1, 8, 16, 256>::loads(4, 0) == 0,
+              "loads behind a group's copy");
+
+// 16-bit ones, and the 8 codes of a dword as 16-bit numbers in the order
+// 0 2 4 6 1 3 5 7.
+template <In T>
+__device__ __forceinline__ u32x4 ones() {
+    const uint32_t o = T == In::BF16 ? 0x3f803f80u : 0x3c003c00u;
+    return u32x4{o, o, o, o};
+}
+template <In T>
+__device__ __forceinline__ u32x4 decode8(uint32_t q) {
+    const uint32_t lo = q & 0x0f0f0f0fu, hi = (q >> 4) & 0x0f0f0f0fu;
+    if constexpr (T == In::BF16) {
+        return u32x4{
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true))};
+    } else {
+        return u32x4{
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true))};
+    }
+}
+// Eight activations in that order.
+__device__ __forceinline__ u32x4 even_odd(const u32x4& x) {
+    return u32x4{(x[0] & 0xffffu) | (x[1] << 16), (x[2] & 0xffffu) | (x[3] << 16),
+                 (x[0] >> 16) | (x[1] & 0xffff0000u), (x[2] >> 16) | (x[3] & 0xffff0000u)};
+}
+
+// One 16-byte piece per lane into LDS (lane l's bytes at lds + 16*l).
+__device__ __forceinline__ void copy_piece(const void* base, uint32_t range, uint8_t* lds,
+                                           uint32_t voff) {
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, range, kBufferRsrcW3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (dma::lds_void*)lds, 16, voff, 0, 0, kBPolicy);
+}
+
+template <In T, typename G>
+__global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, int mchunks) {
+    constexpr bool kW4 = G::kW4, kGated = G::kGated;
+    constexpr int RB = G::RB, NG = G::NG, GR = G::GR, ROWB = G::ROWB, NS = G::NS, D = G::D, P = G::P,
+                  CB = G::CB, NBK = G::NBK, STAGE = G::STAGE, GPS = G::GPS, GB = G::GB;
+    // One object per stage, so that the compiler's wait-count pass can tell a
+    // copy into one from reads of another.
+    __shared__ __attribute__((aligned(256))) uint8_t st0[NW * STAGE];
+    __shared__ __attribute__((aligned(256))) uint8_t st1[NW * STAGE];
+    __shared__ __attribute__((aligned(256))) uint8_t st2[NW * STAGE];
+    __shared__ __attribute__((aligned(256))) uint8_t st3[NW * STAGE];
+    // A step's scales and zero points, [wave][stored row][group]: a scale as fp32, whose last
+    // 13 bits or more are zero, with the zero point in its last byte.
+    __shared__ __attribute__((aligned(16))) uint32_t factors[kW4 ? NW * G::ROWS * GPS : 4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, i = lane & 15;
+    // Workgroups go to the 8 XCDs round-robin: the row chunks of one strip
+    // are 8 apart, so that they run on one XCD and share the weights in its L2.
+    const int q8 = blockIdx.x / (8 * mchunks), r8 = blockIdx.x % (8 * mchunks);
+    const int64_t first = (int64_t)(8 * q8 + r8 % 8) * cols;
+    if (first >= p.N) return;
+    const int n0 = (int)first, nlim = (int)min(first + cols, (int64_t)p.N);
+    const int mbase = (r8 / 8) * 16 * RB;
+    const int rows_x = min(16 * RB, p.M - mbase);
+
+    // group cp's matrix and first output
+    auto matrix = [](int cp) { return kGated ? cp & 1 : 0; };
+    auto out0 = [&](int cp) { return n0 + GR * (kGated ? cp >> 1 : cp); };
+    const uint8_t* gbase[NG];
+    uint32_t grange[NG];
+#pragma unroll
+    for (int cp = 0; cp < NG; ++cp) {
+        const int rows = min(GR, nlim - out0(cp));
+        gbase[cp] = p.W[matrix(cp)] + (int64_t)out0(cp) * p.ldw[matrix(cp)];
+        grange[cp] = rows <= 0 ? 0u
+                               : (uint32_t)((int64_t)(rows - 1) * p.ldw[matrix(cp)] +
+                                            16 * (int64_t)p.chunks);
+    }
+    uint32_t vrow[kGated ? 2 : 1][G::INSTR];
+    int cb[G::INSTR];  // the lane's chunk within the step
+#pragma unroll
+    for (int j = 0; j < G::INSTR; ++j) {
+        const int lr = G::RPI * j + lane / G::LPR;
+        cb[j] = (lane % G::LPR) ^ G::swz(lr);
+#pragma unroll
+        for (int m = 0; m < (kGated ? 2 : 1); ++m) vrow[m][j] = (uint32_t)(lr * p.ldw[m] + 16 * cb[j]);
+    }
+    const int nsteps = (p.chunks + G::CPS - 1) / G::CPS;
+    int s0, s1;
+    skinny::wave_steps(nsteps, NW, wave, s0, s1);
+
+    // rows past M re-read the last one; their sums are not stored
+    const uint16_t* xrow[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+        xrow[rb] = p.X + (int64_t)(mbase + min(16 * rb + i, rows_x - 1)) * p.ldx;
+    const int whole = p.K & ~7;
+
+    floatx4 acc[RB][CB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) acc[rb][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    struct Ops {
+        u32x4 a[RB][P];
+        uint32_t s[kW4 ? G::NSC : 1][G::SW], z[kW4 ? G::NSC : 1][G::ZW];
+    };
+
+    // Copy group cp of step s into ring stage Q (chunks past the row's end, and
+    // steps past the wave's range, read as zeros without memory traffic).
+    auto issue = [&](auto qc, auto cpc, int s) DGT_INLINE {
+        constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
+        uint8_t* dst = dma::pick<Q>(st0, st1, st2, st3) + STAGE * wave;
+        const int lim = s < s1 ? p.chunks - G::CPS * s : 0;
+#pragma unroll
+        for (int j = 0; j < G::INSTR; ++j) {
+            const uint32_t voff =
+                cb[j] < lim ? vrow[matrix(cp)][j] + (uint32_t)(ROWB * s) : grange[cp];
+            copy_piece(gbase[cp], grange[cp], dst + 1024 * j, voff);
+        }
+    };
+    // The lane's rows of scales and zero points: stored row 64j + lane (past the
+    // strip its last one, whose sums are not stored).
+    const uint16_t* srow[kW4 ? G::NSC : 1];
+    const uint8_t* zrow[kW4 ? G::NSC : 1];
+    if constexpr (kW4) {
+#pragma unroll
+        for (int j = 0; j < G::NSC; ++j) {
+            const int r = min(64 * j + lane, G::ROWS - 1), cp = r / GR;
+            const int64_t out = min(out0(cp) + r % GR, nlim - 1);
+            srow[j] = (matrix(cp) ? p.S[1] : p.S[0]) + out * p.lds;
+            zrow[j] = p.Z[0] ? (matrix(cp) ? p.Z[1] : p.Z[0]) + out * p.ldz : p.W[0];
+        }
+    }
+    const bool few = p.groups < GPS;  // then there is one step
+    // First k of the lane's product e in a step, from 8*GB*g on.
+    auto piece = [](int e) { return 32 * GB * (e / GB) + 8 * (e % GB); };
+    // First scale group to load in step s: the step's, or where the row ends in
+    // it the last ones of the row.
+    auto group_at = [&](int s) DGT_INLINE { return min(GPS * s, p.groups - GPS); };
+    // Activations, scales and zero points of step s (past the last step: the last one's):
+    // LA vector loads, which the waits below count on.  What the row does not have (activations
+    // past K; scales where there are fewer than a step's, zero points where none are stored)
+    // is loaded from the weight's first bytes and replaced later.
+    auto load_ops = [&](int s, Ops& o) DGT_INLINE {
+        s = min(s, nsteps - 1);
+        const int k0 = G::KS * s + 8 * GB * g;
+        if (G::KS * (s + 1) <= p.K) {  // uniform
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(xrow[rb] + k0 + piece(e));
+                    o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
+                }
+        } else {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const int k = k0 + piece(e);
+                    const void* from = k < whole ? static_cast<const void*>(xrow[rb] + k)
+                                               : static_cast<const void*>(p.W[0]);
+                    const u32x4_any v = *static_cast<const u32x4_any*>(from);
+                    o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
+                }
+        }
+        if constexpr (kW4) {
+            const int at = group_at(s);
+#pragma unroll
+            for (int j = 0; j < G::NSC; ++j) {
+                const void* sp = few ? static_cast<const void*>(p.W[0]) : srow[j] + at;
+                const void* zp = few || !p.Z[0] ? p.W[0] : zrow[j] + at;
+                __builtin_memcpy(o.s[j], sp, 2 * GPS);
+                __builtin_memcpy(o.z[j], zp, GPS);
+            }
+        }
+    };
+    // The scales and zero points of a row with fewer groups than a step.
+    auto load_few = [&](Ops& o) DGT_INLINE {
+#pragma unroll
+        for (int j = 0; j < G::NSC; ++j) {
+#pragma unroll
+            for (int d = 0; d < G::SW; ++d) o.s[j][d] = 0u;
+#pragma unroll
+            for (int d = 0; d < G::ZW; ++d) o.z[j][d] = 0u;
+#pragma unroll
+            for (int e = 0; e + 1 < GPS; ++e)
+                if (e < p.groups) {
+                    o.s[j][e / 2] |= (uint32_t)srow[j][e] << (16 * (e % 2));
+                    o.z[j][e / 4] |= (uint32_t)zrow[j][p.Z[0] ? e : 0] << (8 * (e % 4));
+                }
+        }
+    };
+
+    floatx4 xs[RB][kW4 && G::kKeepSums ? GPS : 1];
+    auto sum_x = [&](const Ops& o, int rb, int j) DGT_INLINE {  // of scale group j
+        floatx4 x = floatx4{0.f, 0.f, 0.f, 0.f};
+        // made again, these must not look the same as the last time either
+        if constexpr (!G::kKeepSums) asm volatile("" : "+v"(x));
+#pragma unroll
+        for (int e = GB * j; e < GB * (j + 1); ++e) x = mfma16x16x32<T>(o.a[rb][e], ones<T>(), x);
+        return x;
+    };
+    // Once a step: zeros past K, scales 0 past the last group (their sums are
+    // zero, but what is stored there may be anything); the scales into LDS (this
+    // wave's, and LDS keeps its order); the activations' order (sums do not mind
+    // it), and their sums.
+    const uint32_t smask = p.s_bf16 ? 0xffffffffu : 0u;
+    uint32_t* const fac = factors + (kW4 ? G::ROWS * GPS * wave : 0);
+    auto prepare = [&](int s, Ops& o) DGT_INLINE {
+        if (G::KS * (s + 1) > p.K) {  // uniform
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                u32x4 tail = {0u, 0u, 0u, 0u};  // the row's last elements, fewer than 8
+                if (kW4 && whole < p.K)
+                    tail = skinny::load16_cached<uint16_t, true, true>(xrow[rb], whole, p.K, true);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const int k = G::KS * s + 8 * GB * g + piece(e);
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        o.a[rb][e][d] = k < whole ? o.a[rb][e][d] : k == whole ? tail[d] : 0u;
+                }
+            }
+        }
+        if constexpr (kW4) {
+            const int skip = few ? 0 : GPS * s - group_at(s), left = p.groups - GPS * s;  // uniform
+            const uint32_t no_z = p.Z[0] ? 0u : 0xffffffffu;
+#pragma unroll
+            for (int j = 0; j < G::NSC; ++j) {
+#pragma unroll 1
+                for (int t = 0; t < skip; ++t) {  // groups of the step before
+#pragma unroll
+                    for (int d = 0; d < G::SW; ++d)
+                        o.s[j][d] = (o.s[j][d] >> 16) | (d + 1 < G::SW ? o.s[j][(d + 1) % G::SW] << 16 : 0u);
+#pragma unroll
+                    for (int d = 0; d < G::ZW; ++d)
+                        o.z[j][d] = (o.z[j][d] >> 8) | (d + 1 < G::ZW ? o.z[j][(d + 1) % G::ZW] << 24 : 0u);
+                }
+                uint32_t f[GPS];
+#pragma unroll
+                for (int e = 0; e < GPS; ++e) {
+                    // one of the two values by masks: a branch for each would break up the code
+                    const uint32_t bits = (o.s[j][e / 2] >> (16 * (e % 2))) & 0xffffu;
+                    const uint32_t half = __float_as_uint(w4::scale_value(bits, false));
+                    const uint32_t z = (o.z[j][e / 4] >> (8 * (e % 4))) & 255u;
+                    f[e] = ((bits << 16) & smask) | (half & ~smask) | (z & ~no_z) | (8u & no_z);
+                    f[e] = e < left ? f[e] : 0u;
+                }
+                if (64 * (j + 1) <= G::ROWS || lane < G::ROWS - 64 * j)
+                    __builtin_memcpy(__builtin_assume_aligned(fac + (64 * j + lane) * GPS,
+                                                              GPS >= 4 ? 16 : 4 * GPS),
+                                     f, 4 * GPS);
+            }
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) o.a[rb][e] = even_odd(o.a[rb][e]);
+                if constexpr (G::kKeepSums) {
+#pragma unroll
+                    for (int j = 0; j < GPS; ++j) xs[rb][j] = sum_x(o, rb, j);
+                }
+            }
+        }
+    };
+    // Byte of the lane's first chunk in a group's stage, row i; chunks further on by
+    // a power of two differ in one bit of the swizzled place, and 16 rows further
+    // on the swizzle is the same.
+    const uint32_t lds_at =
+        kW4 ? (uint32_t)(i * ROWB + (((GB * g / 4) ^ G::swz(i)) << 4) + 4 * GB * g % 16)
+            : (uint32_t)(i * ROWB + ((g ^ G::swz(i)) << 4));
+    static_assert(kW4 || GB == 1, "16-bit weights have no groups");
+    auto compute = [&](auto qc, auto cpc, const Ops& o) DGT_INLINE {
+        constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
+        const uint8_t* st = dma::pick<Q>(st0, st1, st2, st3) + STAGE * wave;
+        // not known to the compiler to be the same every time: it would keep
+        // every address made from it in a register of its own
+        uint32_t at = lds_at;
+        asm volatile("" : "+v"(at));
+        if constexpr (kW4) {
+            uint32_t q[NBK][P];
+#pragma unroll
+            for (int b = 0; b < NBK; ++b)
+#pragma unroll
+                for (int u = 0; u < GPS; ++u)
+                    __builtin_memcpy(q[b] + GB * u,
+                                     __builtin_assume_aligned(
+                                         st + (at ^ (16 * GB * u)) + 16 * b * ROWB, 4 * GB),
+                                     4 * GB);
+            uint32_t f[NBK][GPS];
+#pragma unroll
+            for (int b = 0; b < NBK; ++b)
+                __builtin_memcpy(f[b],
+                                 __builtin_assume_aligned(fac + (GR * cp + 16 * b + i) * GPS,
+                                                          GPS >= 4 ? 16 : 4 * GPS),
+                                 4 * GPS);
+            __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead of the products
+#pragma unroll
+            for (int j = 0; j < GPS; ++j) {
+                floatx4 x[RB];
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    if constexpr (G::kKeepSums) x[rb] = xs[rb][j];
+                    else x[rb] = sum_x(o, rb, j);
+                }
+#pragma unroll
+                for (int b = 0; b < NBK; ++b) {
+                    constexpr int c0 = NBK * cp;
+                    floatx4 sum[RB];
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) sum[rb] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = GB * j; e < GB * (j + 1); ++e) {
+                        const u32x4 w = decode8<T>(q[b][e]);
+#pragma unroll
+                        for (int rb = 0; rb < RB; ++rb) sum[rb] = mfma16x16x32<T>(o.a[rb][e], w, sum[rb]);
+                    }
+                    const float sc = __uint_as_float(f[b][j] & 0xffffff00u);
+                    const float z = (float)(f[b][j] & 255u);
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[rb][c0 + b][r] =
+                                fmaf(sc, fmaf(-z, x[rb][r], sum[rb][r]), acc[rb][c0 + b][r]);
+                }
+                // a few products at a time: all at once do not fit the registers
+                if (GB * (j + 1) % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            u32x4 w[NBK][P];
+#pragma unroll
+            for (int b = 0; b < NBK; ++b)
+#pragma unroll
+                for (int e = 0; e < P; ++e)
+                    w[b][e] = *reinterpret_cast<const u32x4*>(st + (at ^ (64 * e)) + 16 * b * ROWB);
+            __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead of the products
+#pragma unroll
+            for (int b = 0; b < NBK; ++b)
+#pragma unroll
+                for (int e = 0; e < P; ++e)
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb)
+                        acc[rb][NBK * cp + b] =
+                            mfma16x16x32<T>(o.a[rb][e], w[b][e], acc[rb][NBK * cp + b]);
+        }
+    };
+    auto fence = [] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // Group cp of step s, in ring stage Q.  The wave first copies the group D
+    // places ahead (in phase 0 it then loads the next step's operands), then
+    // waits until its own copy of this group has landed: newer are the D
+    // groups' copies after it, and the loads of operands in the phases since (G::loads).
+    auto phase = [&](auto qc, auto cpc, int s, Ops& o, Ops& next) DGT_INLINE {
+        constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
+        constexpr int ahead = cp + D;
+        DMA_WAIT_VMCNT_LGKM0(63);  // this wave's reads of the stage have returned
+        issue(std::integral_constant<int, (Q + D) % NS>{}, std::integral_constant<int, ahead % NG>{},
+              s + ahead / NG);
+        fence();
+        if constexpr (cp == 0) {
+            load_ops(s + 1, next);
+            fence();
+        }
+        static_for<G::kFirst + 1>([&](auto tc) DGT_INLINE {
+            constexpr int t = decltype(tc)::value;
+            constexpr int after = G::INSTR * D + G::LA * G::loads(cp, t);
+            if (t == G::kFirst ? s - s0 >= t : s - s0 == t) {  // uniform
+                DMA_WAIT_VMCNT((after < 63 ? after : 63));
+            }
+        });
+        fence();
+        if constexpr (cp == 0) prepare(s, o);
+        compute(qc, cpc, o);
+        fence();
+    };
+    // A step whose groups start at ring stage Q0.
+    auto step = [&](auto q0c, int s, Ops& o, Ops& next) DGT_INLINE {
+        constexpr int Q0 = decltype(q0c)::value;
+        static_for<NG>([&](auto cpc) DGT_INLINE {
+            phase(std::integral_constant<int, (Q0 + decltype(cpc)::value) % NS>{}, cpc, s, o, next);
+        });
+    };
+
+    if (s0 < s1) {
+        Ops o0, o1;
+        load_ops(s0, o0);
+        if constexpr (kW4) {
+            if (few) load_few(o0);
+        }
+        fence();
+        static_for<D>([&](auto dc) DGT_INLINE {
+            constexpr int d = decltype(dc)::value;
+            issue(dc, std::integral_constant<int, d % NG>{}, s0 + d / NG);
+        });
+        fence();
+        // Unrolled so that ring stages and operand buffers are compile-time.
+        constexpr int kRing = NS > NG ? NS / NG : 1;
+        constexpr int kUnroll = kRing > 2 ? kRing : 2;
+        for (int s = s0; s < s1; s += kUnroll) {
+            static_for<kUnroll>([&](auto jc) DGT_INLINE {
+                constexpr int j = decltype(jc)::value;
+                if (s + j >= s1) return;
+                using Q0 = std::integral_constant<int, (j * NG) % NS>;
+                if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1);
+                else step(Q0{}, s + j, o1, o0);
+            });
+        }
+    }
+    DMA_WAIT_VMCNT_LGKM0(0);  // every copy has landed: the stages can be reused
+
+    // Partial tiles summed in wave order, RR rows at a time, in stage 0: wave
+    // w's row at (RR*w + row)*ROWS, stored row 16c + i of the strip at
+    // (16c + i) ^ (kSwz * (row/4)), which spreads a write's four row quarters over banks.
+    constexpr int RR = G::RR, ROWS = G::ROWS;
+    constexpr int kSwz = ROWS >= 64 ? 16 : 0;
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(st0);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int hh = 0; hh < 16 / RR; ++hh) {
+            if (16 * rb + RR * hh >= rows_x) continue;  // uniform
+            if (rb + hh) __syncthreads();  // the previous pass's sums have been read
+            if ((4 * g) / RR == hh) {
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        red[(RR * wave + 4 * g + r - RR * hh) * ROWS + ((16 * c + i) ^ (kSwz * g))] =
+                            acc[rb][c][r];
+            }
+            __syncthreads();
+            for (int o = threadIdx.x; o < RR * G::COLS; o += NW * 64) {
+                const int row = o / G::COLS, cl = o % G::COLS, grow = RR * hh + row;
+                const int m = 16 * rb + grow, n = n0 + cl;
+                if (m >= rows_x || n >= nlim) continue;
+                auto total = [&](int stored) DGT_INLINE {
+                    const int at = row * ROWS + (stored ^ (kSwz * ((grow >> 2) & 3)));
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) sum += red[RR * ROWS * w + at];
+                    return sum;
+                };
+                const int64_t mm = mbase + m;
+                if constexpr (kGated) {
+                    const int at = 2 * GR * (cl / GR) + cl % GR;  // its row in an even group
+                    float x = total(at), u = total(at + GR);
+                    if (p.bg) x += p.bg[n];
+                    if (p.bu) u += p.bu[n];
+                    p.H[mm * p.ldh + n] = gated::to_bits<T>(gated::act_of(p.act, x) * u);
+                    if (p.G) p.G[mm * p.ldg + n] = gated::to_bits<T>(x);
+                    if (p.U) p.U[mm * p.ldu + n] = gated::to_bits<T>(u);
+                } else {
+                    float* c = p.C + mm * p.ldc + n;
+                    const float sum = total(cl);
+                    const float r = p.beta == 0.0f ? p.alpha * sum : p.alpha * sum + p.beta * *c;
+                    *c = p.bias ? r + p.bias[n] : r;
+                }
+            }
+        }
+}
+
+// Strips as narrow as the number of rounds of the CUs (a workgroup each) that the widest
+// would take allows.
+template <In T, typename G>
+hipError_t launch(const Params& p, hipStream_t s) {
+    const int64_t mchunks = ((int64_t)p.M + 16 * G::RB - 1) / (16 * G::RB);
+    const int64_t rounds = (((int64_t)p.N + G::COLS - 1) / G::COLS + dma::kCUs - 1) / dma::kCUs;
+    const int cols = (int)(((int64_t)p.N + rounds * dma::kCUs - 1) / (rounds * dma::kCUs));
+    const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
+    const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
+    if (wgs >= (int64_t(1) << 32) / (NW * 64)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((strip_kernel<T, G>), dim3((unsigned)wgs), dim3(NW * 64), 0, s, p, cols,
+                       (int)mchunks);
+    return hipGetLastError();
+}
+
+}  // namespace strip
+}  // namespace dgt
