@@ -13,9 +13,14 @@ using strip::Cfg;
 template <In T, int LG, bool kGated>
 hipError_t launch_group(const strip::Params& p, hipStream_t s) {
     constexpr int kPair = kGated ? 2 : 1;
-    if (p.M > 16) return strip::launch<T, Cfg<true, LG, kGated, 2, 4, 16, 128>>(p, s);
-    if (p.N <= 16 * dma::kCUs) return strip::launch<T, Cfg<true, LG, kGated, 1, kPair, 16, 128>>(p, s);
-    return strip::launch<T, Cfg<true, LG, kGated, 1, LG == 2 ? 4 : 2, 32, 128>>(p, s);
+    constexpr int64_t kCUs = dma::kCUs;
+    if (p.M > 16 && p.N > 32 * kCUs) return strip::launch<T, Cfg<true, LG, kGated, 2, 4, 32, 128>>(p, s);
+    if (p.N <= 16 * kCUs) return strip::launch<T, Cfg<true, LG, kGated, 1, kPair, 16, 128>>(p, s);
+    if constexpr (!kGated) {
+        if (p.N <= 32 * kCUs) return strip::launch<T, Cfg<true, LG, false, 1, 2, 16, 128>>(p, s);
+    }
+    if (p.N <= 64 / kPair * kCUs) return strip::launch<T, Cfg<true, LG, kGated, 1, 4, 16, 128>>(p, s);
+    return strip::launch<T, Cfg<true, LG, kGated, 1, 8, 16, 128>>(p, s);
 }
 
 template <bool kGated>

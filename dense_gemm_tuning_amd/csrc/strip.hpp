@@ -23,8 +23,9 @@
 // conversion gives the codes themselves, exactly, two per instruction; no
 // weight is rounded.  The even codes of a dword come from its low halves of bytes and the
 // odd ones from the high halves, so the activations are put into the order 0 2 4 6 1 3
-// 5 7 once a step.  Per group the products sum x*q, and sum x (a product with ones, once
-// for all rows of the strip), are joined as acc += s * (sum xq - z * sum x).
+// 5 7 once a step.  Per group acc += s * (sum xq - z * sum x), with sum x a product
+// with ones, once for all rows of the strip, or (kKeepSums) with -z inside the
+// same sum.
 #pragma once
 
 #include "dma_common.hpp"
@@ -66,7 +67,8 @@ struct Params {
 };
 
 // kW4: 4-bit weights, 2^LG blocks of 32 k a scale group.
-template <bool kW4_, int LG_, bool kGated_, int RB_, int NG_, int GR_, int ROWB_>
+template <bool kW4_, int LG_, bool kGated_, int RB_, int NG_, int GR_, int ROWB_,
+          bool kSingle_ = (kW4_ && RB_ > 1)>
 struct Cfg {
     static constexpr bool kW4 = kW4_, kGated = kGated_;
     static constexpr int RB = RB_, NG = NG_, GR = GR_, ROWB = ROWB_;
@@ -82,29 +84,44 @@ struct Cfg {
     static constexpr int INSTR = STAGE / 1024, RPI = 1024 / ROWB, LPR = ROWB / 16;
     static constexpr int GB = 1 << LG_;                   // blocks per scale group
     static constexpr int GPS = kW4 ? P / GB : 1;          // scale groups per step
-    // Scales and zero points: a lane loads a step's of one stored row (GPS
-    // 16-bit values and GPS bytes), a step ahead.
+    // Scales and zero points: a lane loads kRun groups' of one stored row at a time (16
+    // and 8 bytes), SPS steps' worth, a step ahead.  (A row's next groups lie in the
+    // same cache line, but the streamed weights drive it out of L1 between steps: two
+    // groups at a time fetched more bytes of scales than of codes.)
+    static constexpr int kRun = 8, SPS = kRun / GPS;
+    static_assert(!kW4 || SPS * GPS == kRun, "a run is whole steps");
     static constexpr int NSC = kW4 ? (ROWS + 63) / 64 : 0;
-    static constexpr int SW = (GPS + 1) / 2, ZW = (GPS + 3) / 4;  // in dwords
-    static constexpr int LA = RB * P + 2 * NSC;  // vector loads per step besides the copies
-    // Whether the activations' sums per scale group are kept for the step, or
-    // made again for every group of rows (their registers are many when the scale groups are).
+    // Vector loads per step besides the copies (those of scales where every
+    // step has them; elsewhere they are not counted, which only waits for more).
+    static constexpr int LA = RB * P + (SPS == 1 ? 2 * NSC : 0);
+    // Activations in one buffer, loaded again behind a step's last products (with
+    // more rows two do not fit the registers), or in two, a step ahead.
+    static constexpr bool kSingle = kSingle_;
+    // Whether the activations' sums per scale group are made once a step and kept, or
+    // (their registers are many when the scale groups are) the products with
+    // the zero point are added up with those with the codes.
     static constexpr bool kKeepSums = RB * GPS <= 4;
     // rows of a reduction pass in one stage of all waves
     static constexpr int RR = STAGE / (ROWS * 4) < 16 ? STAGE / (ROWS * 4) : 16;
-    static_assert(ROWB == 256 || ROWB == 128, "a row piece is 256 or 128 bytes");
+    static_assert(ROWB == 256 || ROWB == 128 || ROWB == 64, "a row piece is 256, 128 or 64 bytes");
     static_assert(NG == 1 || NG == 2 || NG == 4 || NG == 8, "groups map onto the ring");
     static_assert(!kGated || NG % 2 == 0, "a gated strip's groups come in pairs");
     static_assert(!kW4 || P % GB == 0, "a scale group does not cross steps");
     static_assert(RR >= 4, "a pass holds an accumulator's rows");
-    __device__ static int swz(int r) { return ROWB == 256 ? (r & 15) : ((r >> 1) & 7); }
-    // Loads of operands (one in each phase 0) from the phase that copied group cp of the
-    // wave's step t, D phases before, to that group's: in the first kFirst steps
-    // some of those phases are the prologue, which loads before it copies.
+    __device__ static int swz(int r) {  // 256 / ROWB rows share a line of all banks
+        return ROWB == 256 ? (r & 15) : ROWB == 128 ? ((r >> 1) & 7) : ((r >> 2) & 3);
+    }
+    // Loads of operands behind the copy of group cp of the wave's step t, D phases
+    // before that group's wait: one in each phase 0 behind its copy, or with one buffer at
+    // the end of each step.  In the first kFirst steps some of those phases are the
+    // prologue, which loads before it copies (with one buffer, after).
     static constexpr int kFirst = NG >= D + 1 ? 0 : (D + NG - 1) / NG;
     static constexpr int loads(int cp, int t) {
         int n = 0;
-        for (int x = cp - D < -t * NG ? -t * NG : cp - D; x <= cp; ++x) n += x % NG == 0;
+        for (int x = cp - D; x <= cp; ++x) {
+            if (kSingle) n += x < cp && x >= -t * NG - 1 && (x + 8 * NG) % NG == NG - 1;
+            else n += x >= -t * NG && x % NG == 0;
+        }
         return n;
     }
 };
@@ -144,8 +161,9 @@ __device__ __forceinline__ u32x4 decode8(uint32_t q) {
 }
 // Eight activations in that order.
 __device__ __forceinline__ u32x4 even_odd(const u32x4& x) {
-    return u32x4{(x[0] & 0xffffu) | (x[1] << 16), (x[2] & 0xffffu) | (x[3] << 16),
-                 (x[0] >> 16) | (x[1] & 0xffff0000u), (x[2] >> 16) | (x[3] & 0xffff0000u)};
+    constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;  // halves of two dwords, side by side
+    return u32x4{__builtin_amdgcn_perm(x[1], x[0], kLow), __builtin_amdgcn_perm(x[3], x[2], kLow),
+                 __builtin_amdgcn_perm(x[1], x[0], kHigh), __builtin_amdgcn_perm(x[3], x[2], kHigh)};
 }
 
 // One 16-byte piece per lane into LDS (lane l's bytes at lds + 16*l).
@@ -167,9 +185,9 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
     __shared__ __attribute__((aligned(256))) uint8_t st1[NW * STAGE];
     __shared__ __attribute__((aligned(256))) uint8_t st2[NW * STAGE];
     __shared__ __attribute__((aligned(256))) uint8_t st3[NW * STAGE];
-    // A step's scales and zero points, [wave][stored row][group]: a scale as fp32, whose last
+    // A run's scales and zero points, [wave][stored row][group]: a scale as fp32, whose last
     // 13 bits or more are zero, with the zero point in its last byte.
-    __shared__ __attribute__((aligned(16))) uint32_t factors[kW4 ? NW * G::ROWS * GPS : 4];
+    __shared__ __attribute__((aligned(16))) uint32_t factors[kW4 ? NW * G::ROWS * G::kRun : 4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, i = lane & 15;
@@ -223,7 +241,9 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
 
     struct Ops {
         u32x4 a[RB][P];
-        uint32_t s[kW4 ? G::NSC : 1][G::SW], z[kW4 ? G::NSC : 1][G::ZW];
+    };
+    struct Scales {
+        uint32_t s[kW4 ? G::NSC : 1][G::kRun / 2], z[kW4 ? G::NSC : 1][G::kRun / 4];
     };
 
     // Copy group cp of step s into ring stage Q (chunks past the row's end, and
@@ -239,6 +259,7 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
             copy_piece(gbase[cp], grange[cp], dst + 1024 * j, voff);
         }
     };
+
     // The lane's rows of scales and zero points: stored row 64j + lane (past the
     // strip its last one, whose sums are not stored).
     const uint16_t* srow[kW4 ? G::NSC : 1];
@@ -252,27 +273,28 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
             zrow[j] = p.Z[0] ? (matrix(cp) ? p.Z[1] : p.Z[0]) + out * p.ldz : p.W[0];
         }
     }
-    const bool few = p.groups < GPS;  // then there is one step
     // First k of the lane's product e in a step, from 8*GB*g on.
     auto piece = [](int e) { return 32 * GB * (e / GB) + 8 * (e % GB); };
-    // First scale group to load in step s: the step's, or where the row ends in
-    // it the last ones of the row.
-    auto group_at = [&](int s) DGT_INLINE { return min(GPS * s, p.groups - GPS); };
-    // Activations, scales and zero points of step s (past the last step: the last one's):
-    // LA vector loads, which the waits below count on.  What the row does not have (activations
-    // past K; scales where there are fewer than a step's, zero points where none are stored)
-    // is loaded from the weight's first bytes and replaced later.
+    const bool few = p.groups < G::kRun;  // then no wave has more than a run
+    // First scale group to load for the run that starts with step s: its own, or where the
+    // row ends in it the last ones of the row.
+    auto group_at = [&](int s) DGT_INLINE { return min(GPS * s, p.groups - G::kRun); };
+    // Activations of step s (past the last step: the last one's): RB*P vector
+    // loads, which the waits below count on.  What lies past K is loaded from the weight's first
+    // bytes and replaced in `prepare`.
     auto load_ops = [&](int s, Ops& o) DGT_INLINE {
         s = min(s, nsteps - 1);
         const int k0 = G::KS * s + 8 * GB * g;
         if (G::KS * (s + 1) <= p.K) {  // uniform
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
+            for (int rb = 0; rb < RB; ++rb) {
+                const uint16_t* from = xrow[rb] + k0;
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
-                    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(xrow[rb] + k0 + piece(e));
+                    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from + piece(e));
                     o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
                 }
+            }
         } else {
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb)
@@ -280,32 +302,34 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
                 for (int e = 0; e < P; ++e) {
                     const int k = k0 + piece(e);
                     const void* from = k < whole ? static_cast<const void*>(xrow[rb] + k)
-                                               : static_cast<const void*>(p.W[0]);
+                                                 : static_cast<const void*>(p.W[0]);
                     const u32x4_any v = *static_cast<const u32x4_any*>(from);
                     o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
+                    asm volatile("" ::: "memory");  // one address at a time
                 }
         }
-        if constexpr (kW4) {
-            const int at = group_at(s);
+    };
+    // The run of scales and zero points from step s on (none of the row's where
+    // there are fewer or no zero points: then replaced in `prepare`).
+    auto load_scales = [&](int s, Scales& o) DGT_INLINE {
+        const int at = group_at(min(s, nsteps - 1));
 #pragma unroll
-            for (int j = 0; j < G::NSC; ++j) {
-                const void* sp = few ? static_cast<const void*>(p.W[0]) : srow[j] + at;
-                const void* zp = few || !p.Z[0] ? p.W[0] : zrow[j] + at;
-                __builtin_memcpy(o.s[j], sp, 2 * GPS);
-                __builtin_memcpy(o.z[j], zp, GPS);
-            }
+        for (int j = 0; j < G::NSC; ++j) {
+            const void* sp = few ? static_cast<const void*>(p.W[0]) : srow[j] + at;
+            const void* zp = few || !p.Z[0] ? p.W[0] : zrow[j] + at;
+            __builtin_memcpy(o.s[j], sp, 2 * G::kRun);
+            __builtin_memcpy(o.z[j], zp, G::kRun);
         }
     };
-    // The scales and zero points of a row with fewer groups than a step.
-    auto load_few = [&](Ops& o) DGT_INLINE {
+    auto load_few = [&](Scales& o) DGT_INLINE {
 #pragma unroll
         for (int j = 0; j < G::NSC; ++j) {
 #pragma unroll
-            for (int d = 0; d < G::SW; ++d) o.s[j][d] = 0u;
+            for (int d = 0; d < G::kRun / 2; ++d) o.s[j][d] = 0u;
 #pragma unroll
-            for (int d = 0; d < G::ZW; ++d) o.z[j][d] = 0u;
+            for (int d = 0; d < G::kRun / 4; ++d) o.z[j][d] = 0u;
 #pragma unroll
-            for (int e = 0; e + 1 < GPS; ++e)
+            for (int e = 0; e + 1 < G::kRun; ++e)
                 if (e < p.groups) {
                     o.s[j][e / 2] |= (uint32_t)srow[j][e] << (16 * (e % 2));
                     o.z[j][e / 4] |= (uint32_t)zrow[j][p.Z[0] ? e : 0] << (8 * (e % 4));
@@ -314,20 +338,44 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
     };
 
     floatx4 xs[RB][kW4 && G::kKeepSums ? GPS : 1];
-    auto sum_x = [&](const Ops& o, int rb, int j) DGT_INLINE {  // of scale group j
-        floatx4 x = floatx4{0.f, 0.f, 0.f, 0.f};
-        // made again, these must not look the same as the last time either
-        if constexpr (!G::kKeepSums) asm volatile("" : "+v"(x));
-#pragma unroll
-        for (int e = GB * j; e < GB * (j + 1); ++e) x = mfma16x16x32<T>(o.a[rb][e], ones<T>(), x);
-        return x;
-    };
-    // Once a step: zeros past K, scales 0 past the last group (their sums are
-    // zero, but what is stored there may be anything); the scales into LDS (this
-    // wave's, and LDS keeps its order); the activations' order (sums do not mind
-    // it), and their sums.
+    // A run of scales into LDS (this wave's part, and LDS keeps its order); past
+    // the row's last group scales of 0: its sums are zero, but what is stored there
+    // may be anything.
     const uint32_t smask = p.s_bf16 ? 0xffffffffu : 0u;
-    uint32_t* const fac = factors + (kW4 ? G::ROWS * GPS * wave : 0);
+    uint32_t* const fac = factors + (kW4 ? G::ROWS * G::kRun * wave : 0);
+    auto put_scales = [&](int s, Scales& o) DGT_INLINE {
+        constexpr int SW = G::kRun / 2, ZW = G::kRun / 4;
+        const int skip = GPS * s - (few ? 0 : group_at(s)), left = p.groups - GPS * s;  // uniform
+        const uint32_t no_z = p.Z[0] ? 0u : 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < G::NSC; ++j) {
+#pragma unroll 1
+            for (int t = 0; t < skip; ++t) {  // groups before the run
+#pragma unroll
+                for (int d = 0; d < SW; ++d)
+                    o.s[j][d] = (o.s[j][d] >> 16) | (d + 1 < SW ? o.s[j][(d + 1) % SW] << 16 : 0u);
+#pragma unroll
+                for (int d = 0; d < ZW; ++d)
+                    o.z[j][d] = (o.z[j][d] >> 8) | (d + 1 < ZW ? o.z[j][(d + 1) % ZW] << 24 : 0u);
+            }
+            uint32_t f[G::kRun];
+#pragma unroll
+            for (int e = 0; e < G::kRun; ++e) {
+                // one of the two values by masks: a branch for each would break up the code
+                const uint32_t bits = (o.s[j][e / 2] >> (16 * (e % 2))) & 0xffffu;
+                const uint32_t half = __float_as_uint(w4::scale_value(bits, false));
+                const uint32_t z = (o.z[j][e / 4] >> (8 * (e % 4))) & 255u;
+                f[e] = ((bits << 16) & smask) | (half & ~smask) | (z & ~no_z) | (8u & no_z);
+                f[e] = e < left ? f[e] : 0u;
+            }
+            if (64 * (j + 1) <= G::ROWS || lane < G::ROWS - 64 * j)
+                __builtin_memcpy(__builtin_assume_aligned(fac + (64 * j + lane) * G::kRun, 16), f,
+                                 4 * G::kRun);
+        }
+        asm volatile("" ::: "memory");
+    };
+    // Once a step: zeros past K; the activations' order (sums do not mind it),
+    // and their sums.
     auto prepare = [&](int s, Ops& o) DGT_INLINE {
         if (G::KS * (s + 1) > p.K) {  // uniform
 #pragma unroll
@@ -345,42 +393,16 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
             }
         }
         if constexpr (kW4) {
-            const int skip = few ? 0 : GPS * s - group_at(s), left = p.groups - GPS * s;  // uniform
-            const uint32_t no_z = p.Z[0] ? 0u : 0xffffffffu;
-#pragma unroll
-            for (int j = 0; j < G::NSC; ++j) {
-#pragma unroll 1
-                for (int t = 0; t < skip; ++t) {  // groups of the step before
-#pragma unroll
-                    for (int d = 0; d < G::SW; ++d)
-                        o.s[j][d] = (o.s[j][d] >> 16) | (d + 1 < G::SW ? o.s[j][(d + 1) % G::SW] << 16 : 0u);
-#pragma unroll
-                    for (int d = 0; d < G::ZW; ++d)
-                        o.z[j][d] = (o.z[j][d] >> 8) | (d + 1 < G::ZW ? o.z[j][(d + 1) % G::ZW] << 24 : 0u);
-                }
-                uint32_t f[GPS];
-#pragma unroll
-                for (int e = 0; e < GPS; ++e) {
-                    // one of the two values by masks: a branch for each would break up the code
-                    const uint32_t bits = (o.s[j][e / 2] >> (16 * (e % 2))) & 0xffffu;
-                    const uint32_t half = __float_as_uint(w4::scale_value(bits, false));
-                    const uint32_t z = (o.z[j][e / 4] >> (8 * (e % 4))) & 255u;
-                    f[e] = ((bits << 16) & smask) | (half & ~smask) | (z & ~no_z) | (8u & no_z);
-                    f[e] = e < left ? f[e] : 0u;
-                }
-                if (64 * (j + 1) <= G::ROWS || lane < G::ROWS - 64 * j)
-                    __builtin_memcpy(__builtin_assume_aligned(fac + (64 * j + lane) * GPS,
-                                                              GPS >= 4 ? 16 : 4 * GPS),
-                                     f, 4 * GPS);
-            }
-            asm volatile("" ::: "memory");
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
                 for (int e = 0; e < P; ++e) o.a[rb][e] = even_odd(o.a[rb][e]);
                 if constexpr (G::kKeepSums) {
 #pragma unroll
-                    for (int j = 0; j < GPS; ++j) xs[rb][j] = sum_x(o, rb, j);
+                    for (int j = 0; j < GPS; ++j) xs[rb][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < P; ++e)
+                        xs[rb][e / GB] = mfma16x16x32<T>(o.a[rb][e], ones<T>(), xs[rb][e / GB]);
                 }
             }
         }
@@ -392,7 +414,7 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
         kW4 ? (uint32_t)(i * ROWB + (((GB * g / 4) ^ G::swz(i)) << 4) + 4 * GB * g % 16)
             : (uint32_t)(i * ROWB + ((g ^ G::swz(i)) << 4));
     static_assert(kW4 || GB == 1, "16-bit weights have no groups");
-    auto compute = [&](auto qc, auto cpc, const Ops& o) DGT_INLINE {
+    auto compute = [&](auto qc, auto cpc, int s, const Ops& o) DGT_INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         const uint8_t* st = dma::pick<Q>(st0, st1, st2, st3) + STAGE * wave;
         // not known to the compiler to be the same every time: it would keep
@@ -413,38 +435,47 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
 #pragma unroll
             for (int b = 0; b < NBK; ++b)
                 __builtin_memcpy(f[b],
-                                 __builtin_assume_aligned(fac + (GR * cp + 16 * b + i) * GPS,
-                                                          GPS >= 4 ? 16 : 4 * GPS),
+                                 __builtin_assume_aligned(
+                                     fac + (GR * cp + 16 * b + i) * G::kRun + GPS * ((s - s0) % G::SPS),
+                                     GPS >= 4 ? 16 : 4 * GPS),
                                  4 * GPS);
             __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead of the products
 #pragma unroll
             for (int j = 0; j < GPS; ++j) {
-                floatx4 x[RB];
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    if constexpr (G::kKeepSums) x[rb] = xs[rb][j];
-                    else x[rb] = sum_x(o, rb, j);
-                }
 #pragma unroll
                 for (int b = 0; b < NBK; ++b) {
                     constexpr int c0 = NBK * cp;
+                    const float sc = __uint_as_float(f[b][j] & 0xffffff00u);
+                    const float z = (float)(f[b][j] & 255u);
                     floatx4 sum[RB];
 #pragma unroll
                     for (int rb = 0; rb < RB; ++rb) sum[rb] = floatx4{0.f, 0.f, 0.f, 0.f};
+                    if constexpr (!G::kKeepSums) {
+                        const uint32_t nz = gated::to_bits<T>(-z), pair = nz | (nz << 16);
+                        const u32x4 w = {pair, pair, pair, pair};
+#pragma unroll
+                        for (int e = GB * j; e < GB * (j + 1); ++e)
+#pragma unroll
+                            for (int rb = 0; rb < RB; ++rb)
+                                sum[rb] = mfma16x16x32<T>(o.a[rb][e], w, sum[rb]);
+                    }
 #pragma unroll
                     for (int e = GB * j; e < GB * (j + 1); ++e) {
                         const u32x4 w = decode8<T>(q[b][e]);
 #pragma unroll
                         for (int rb = 0; rb < RB; ++rb) sum[rb] = mfma16x16x32<T>(o.a[rb][e], w, sum[rb]);
                     }
-                    const float sc = __uint_as_float(f[b][j] & 0xffffff00u);
-                    const float z = (float)(f[b][j] & 255u);
 #pragma unroll
                     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[rb][c0 + b][r] =
-                                fmaf(sc, fmaf(-z, x[rb][r], sum[rb][r]), acc[rb][c0 + b][r]);
+                        for (int r = 0; r < 4; ++r) {
+                            float v = sum[rb][r];
+                            if constexpr (G::kKeepSums) v = fmaf(-z, xs[rb][j][r], v);
+                            acc[rb][c0 + b][r] = fmaf(sc, v, acc[rb][c0 + b][r]);
+                        }
+                    // here and not later: the compiler would keep the groups' sums instead
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) asm volatile("" : "+v"(acc[rb][c0 + b]));
                 }
                 // a few products at a time: all at once do not fit the registers
                 if (GB * (j + 1) % 2 == 0) __builtin_amdgcn_sched_barrier(0);
@@ -476,7 +507,7 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
     // places ahead (in phase 0 it then loads the next step's operands), then
     // waits until its own copy of this group has landed: newer are the D
     // groups' copies after it, and the loads of operands in the phases since (G::loads).
-    auto phase = [&](auto qc, auto cpc, int s, Ops& o, Ops& next) DGT_INLINE {
+    auto phase = [&](auto qc, auto cpc, int s, Ops& o, Ops& next, Scales& sc) DGT_INLINE {
         constexpr int cp = decltype(cpc)::value, Q = decltype(qc)::value;
         constexpr int ahead = cp + D;
         DMA_WAIT_VMCNT_LGKM0(63);  // this wave's reads of the stage have returned
@@ -484,52 +515,82 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
               s + ahead / NG);
         fence();
         if constexpr (cp == 0) {
-            load_ops(s + 1, next);
+            if constexpr (kW4) {
+                if ((s - s0) % G::SPS == 0) put_scales(s, sc);
+                fence();
+            }
+            if constexpr (!G::kSingle) load_ops(s + 1, next);
+            if constexpr (kW4) {
+                if ((s + 1 - s0) % G::SPS == 0) load_scales(s + 1, sc);
+            }
             fence();
         }
         static_for<G::kFirst + 1>([&](auto tc) DGT_INLINE {
             constexpr int t = decltype(tc)::value;
             constexpr int after = G::INSTR * D + G::LA * G::loads(cp, t);
-            if (t == G::kFirst ? s - s0 >= t : s - s0 == t) {  // uniform
+            if (G::kFirst == 0 || (t == G::kFirst ? s - s0 >= t : s - s0 == t)) {  // uniform
                 DMA_WAIT_VMCNT((after < 63 ? after : 63));
             }
         });
         fence();
         if constexpr (cp == 0) prepare(s, o);
-        compute(qc, cpc, o);
+        compute(qc, cpc, s, o);
         fence();
+        if constexpr (G::kSingle && cp == NG - 1) {  // o and next are one buffer
+            load_ops(s + 1, next);
+            fence();
+        }
     };
     // A step whose groups start at ring stage Q0.
-    auto step = [&](auto q0c, int s, Ops& o, Ops& next) DGT_INLINE {
+    auto step = [&](auto q0c, int s, Ops& o, Ops& next, Scales& sc) DGT_INLINE {
         constexpr int Q0 = decltype(q0c)::value;
         static_for<NG>([&](auto cpc) DGT_INLINE {
-            phase(std::integral_constant<int, (Q0 + decltype(cpc)::value) % NS>{}, cpc, s, o, next);
+            phase(std::integral_constant<int, (Q0 + decltype(cpc)::value) % NS>{}, cpc, s, o, next,
+                  sc);
         });
     };
 
     if (s0 < s1) {
-        Ops o0, o1;
-        load_ops(s0, o0);
-        if constexpr (kW4) {
-            if (few) load_few(o0);
-        }
-        fence();
-        static_for<D>([&](auto dc) DGT_INLINE {
-            constexpr int d = decltype(dc)::value;
-            issue(dc, std::integral_constant<int, d % NG>{}, s0 + d / NG);
-        });
-        fence();
+        Scales sc;
+        auto operands = [&](Ops& o) DGT_INLINE {
+            load_ops(s0, o);
+            if constexpr (kW4) {
+                load_scales(s0, sc);
+                if (few) load_few(sc);
+            }
+            fence();
+        };
+        auto copies = [&]() DGT_INLINE {
+            static_for<D>([&](auto dc) DGT_INLINE {
+                constexpr int d = decltype(dc)::value;
+                issue(dc, std::integral_constant<int, d % NG>{}, s0 + d / NG);
+            });
+            fence();
+        };
         // Unrolled so that ring stages and operand buffers are compile-time.
         constexpr int kRing = NS > NG ? NS / NG : 1;
-        constexpr int kUnroll = kRing > 2 ? kRing : 2;
-        for (int s = s0; s < s1; s += kUnroll) {
-            static_for<kUnroll>([&](auto jc) DGT_INLINE {
-                constexpr int j = decltype(jc)::value;
-                if (s + j >= s1) return;
-                using Q0 = std::integral_constant<int, (j * NG) % NS>;
-                if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1);
-                else step(Q0{}, s + j, o1, o0);
-            });
+        constexpr int kUnroll = G::kSingle ? kRing : kRing > 2 ? kRing : 2;
+        auto run = [&](Ops& o0, Ops& o1) DGT_INLINE {
+            for (int s = s0; s < s1; s += kUnroll) {
+                static_for<kUnroll>([&](auto jc) DGT_INLINE {
+                    constexpr int j = decltype(jc)::value;
+                    if (s + j >= s1) return;
+                    using Q0 = std::integral_constant<int, (j * NG) % NS>;
+                    if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1, sc);
+                    else step(Q0{}, s + j, o1, o0, sc);
+                });
+            }
+        };
+        if constexpr (G::kSingle) {
+            Ops o;
+            copies();
+            operands(o);
+            run(o, o);
+        } else {
+            Ops o0, o1;
+            operands(o0);
+            copies();
+            run(o0, o1);
         }
     }
     DMA_WAIT_VMCNT_LGKM0(0);  // every copy has landed: the stages can be reused
