@@ -4,7 +4,7 @@
 //
 // Per group, over its elements and zero: with zero points s = (max - min)/15 and z the
 // whole number nearest to -min/s; without, s = max(max/7, -min/8) and z = 8.
-// The quotients that decide s and z are taken in 64 bits; s is rounded to fp32, then
+// The quotient that s is rounded from is taken in 64 bits; s is rounded to fp32, then
 // to its 16-bit type (past that type's largest value: that value).  q = the
 // whole number nearest to x/s, ties to even, plus z, within 0 .. 15.
 #include "w4.hpp"
@@ -45,13 +45,12 @@ struct Raw {
     }
 };
 
-// The whole number nearest to x/s, ties to even.  fp32's quotient may round onto
-// a half-way value that x/s only comes near; what is left of x under the whole
-// number q is exact (q has few bits and q*s is near x), so comparing it
-// with s/2 decides.  Quotients past 16 need no care: the code is bounded there.
-__device__ __forceinline__ float nearest(float x, float s) {
-    float q = rintf(x / s);
-    const float rest = fmaf(-q, s, x), half = 0.5f * s;
+// The whole number nearest to x/s is q = rint(x * (1/s)) in fp32 unless x/s is half
+// way between two whole numbers, or so near to it that fp32's product is on the
+// other side.  What is left of x under q, rest, is exact (q has few bits and q*s is near x),
+// and |rest| < s/2 says that q is right.  Otherwise this decides, ties to
+// even.  Quotients past 16 need no care: the code is bounded there.
+__device__ __forceinline__ float settle(float q, float rest, float half) {
     const bool odd = ((int)fminf(fmaxf(q, -32.0f), 32.0f) & 1) != 0;
     if (rest > half || (rest == half && odd)) q += 1.0f;
     else if (rest < -half || (rest == -half && odd)) q -= 1.0f;
@@ -69,38 +68,47 @@ __global__ __launch_bounds__(NT) void quantize_kernel(const void* Xv, int64_t ld
     using E = typename InFmt<T>::S;
     const E* X = static_cast<const E*>(Xv);
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
+    const int64_t wave = (int64_t)blockIdx.x * (NT / 64) +
+                         __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t waves = (int64_t)gridDim.x * (NT / 64);
     const int code_end = 32 * (K / 32 + (K % 32 != 0));
+    // row and place in the row of the wavefront's next run, and their steps
+    int64_t row_at = wave / runs_per_row;
+    int at = (int)(wave % runs_per_row);
+    const int64_t row_step = waves / runs_per_row;
+    const int at_step = (int)(waves % runs_per_row);
     for (int64_t r0 = wave; r0 < runs; r0 += waves * UN) {
         Raw<T> x[UN];
+        int64_t rows[UN];
+        int ks[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int64_t run = r0 + waves * i;
-            if (run < runs)
-                x[i].load(X + run / runs_per_row * ldx, (int)(run % runs_per_row) * 512 + 8 * lane,
-                          K, vec);
+            rows[i] = row_at;
+            ks[i] = at * 512 + 8 * lane;
+            if (r0 + waves * i < runs) x[i].load(X + row_at * ldx, ks[i], K, vec);
+            row_at += row_step;
+            at += at_step;
+            if (at >= runs_per_row) at -= runs_per_row, ++row_at;
         }
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int64_t run = r0 + waves * i;
-            if (run >= runs) break;
-            const int64_t row = run / runs_per_row;
-            const int k = (int)(run % runs_per_row) * 512 + 8 * lane;
-            float v[8], top = 0.0f, low = 0.0f;
-            bool finite = true;
+            if (r0 + waves * i >= runs) break;
+            const int64_t row = rows[i];
+            const int k = ks[i];
+            float v[8], top = 0.0f, low = 0.0f, bad = 0.0f;  // bad: NaN with an infinity or a NaN
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[e] = x[i].get(e);
                 top = fmaxf(top, v[e]);
                 low = fminf(low, v[e]);
-                finite = finite && (__float_as_uint(v[e]) & 0x7f800000u) != 0x7f800000u;
+                bad = fmaf(v[e], 0.0f, bad);
             }
             for (int d = 1; d < 1 << (log_group - 3); d *= 2) {
                 top = fmaxf(top, __shfl_xor(top, d));
                 low = fminf(low, __shfl_xor(low, d));
-                finite = __shfl_xor((int)finite, d) && finite;
+                bad += __shfl_xor(bad, d);
             }
+            const bool finite = bad == 0.0f;
             const double hi = top, lo = -(double)low;
             float wide = (float)(Z ? (hi + lo) / 15.0 : fmax(hi / 7.0, lo / 8.0));
             // two roundings, as documented: the compiler would join them into one
@@ -110,14 +118,40 @@ __global__ __launch_bounds__(NT) void quantize_kernel(const void* Xv, int64_t ld
             if (bits == inf) bits = inf - 1;
             const float s = scale_value(bits, s_bf16);
             const float unit = s > 0.0f ? s : 1.0f;  // a group of zeros, or below the type's least
-            const float z = Z ? (float)fmin(rint(lo / (double)unit), 15.0) : 8.0f;
+            // the reciprocal of a scale below 2^-100 may be too large for fp32
+            const float up = unit < 0x1p-100f ? 0x1p64f : 1.0f, su = up * unit;
+            const float inv = __builtin_amdgcn_rcpf(su), half = 0.5f * su;
+            float z = 8.0f;
+            if (Z) {
+                const float q = rintf(-low * up * inv);
+                z = fminf(settle(q, fmaf(-q, su, -low * up), half), 15.0f);
+            }
             if (!finite) bits = inf | 1;
-            uint32_t codes = 0;
+            float q[8], most = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float q = fminf(fmaxf(nearest(v[e], unit) + z, 0.0f), 15.0f);
-                codes |= (k + e < K && finite ? (uint32_t)q : 0u) << (4 * e);
+                v[e] *= up;
+                q[e] = v[e] * inv;
+                if constexpr (T == In::F32) {
+                    q[e] = rintf(q[e]);
+                    most = fmaxf(most, fabsf(fmaf(-q[e], su, v[e])));
+                } else {
+                    // Of 16-bit elements, half ways are common and everything
+                    // else is 2^-19 or more away: with the quotient's error taken
+                    // out they come out as they are.
+                    q[e] = rintf(fmaf(fmaf(-q[e], su, v[e]), inv, q[e]));
+                }
             }
+            if (T == In::F32 && !(most < half)) {  // rare
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[e] = settle(q[e], fmaf(-q[e], su, v[e]), half);
+            }
+            uint32_t codes = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                codes |= (uint32_t)fminf(fmaxf(q[e] + z, 0.0f), 15.0f) << (4 * e);
+            if (!finite) codes = 0;
+            if (k + 8 > K) codes &= k < K ? (1u << (4 * (K - k))) - 1u : 0u;
             if (k < code_end) *reinterpret_cast<uint32_t*>(Q + row * ldq + k / 2) = codes;
             if (k < K && (k & ((1 << log_group) - 1)) == 0) {
                 S[row * lds + (k >> log_group)] = bits;
