@@ -24,7 +24,7 @@ SOURCES = ["gemm_api.cpp", "k_naive.hip", "k_lds.hip", "k_mfma_f32.hip", "k_mfma
            "k_splitk.hip", "mx4_api.cpp", "k_mx4_quant.hip", "k_mx4_tile.hip", "k_mx4_skinny.hip",
            "k_mx4_rows.hip", "orth_api.cpp",
            "k_orth.hip", "k_orth_small.hip", "gated_api.cpp", "k_gated_regs.hip", "k_gated_tile.hip", "k_gated_strip.hip",
-           "k_w4_quant.hip", "k_w4_strip.hip"]
+           "k_w4_quant.hip", "k_w4_strip.hip", "k_w4_rows.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

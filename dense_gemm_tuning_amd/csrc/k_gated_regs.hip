@@ -30,13 +30,17 @@ __device__ __forceinline__ u32x4 load16(const uint16_t* src) {
     return v;
 }
 
-// Elements [at, at + 8) of a row, zeros from `limit` on.
+// Elements [at, at + 8) of a row, zeros from `limit` on.  Every element is loaded, those past the
+// row's end from its last one: loads behind a branch each would wait for one another.
 __device__ __forceinline__ u32x4 gather8(const uint16_t* row, int at, int limit) {
+    uint32_t e[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) e[d] = row[max(min(at + d, limit - 1), 0)];
     u32x4 v;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        const uint32_t lo = at + 2 * d < limit ? row[at + 2 * d] : 0u;
-        const uint32_t hi = at + 2 * d + 1 < limit ? row[at + 2 * d + 1] : 0u;
+        const uint32_t lo = at + 2 * d < limit ? e[2 * d] : 0u;
+        const uint32_t hi = at + 2 * d + 1 < limit ? e[2 * d + 1] : 0u;
         v[d] = lo | (hi << 16);
     }
     return v;

@@ -25,6 +25,9 @@ hipError_t launch_group(const strip::Params& p, hipStream_t s) {
 
 template <bool kGated>
 hipError_t launch_strips(In t, int log_group, const strip::Params& p, hipStream_t s) {
+    const bool wide = (kGated ? 2 : 1) * (int64_t)p.N > 32 * dma::kCUs;
+    if ((p.M > 64 || (p.M > 16 && wide)) && rows_eligible(p))
+        return launch_rows(t, kGated, log_group, p, s);
     auto go = [&](auto tc) {
         constexpr In T = decltype(tc)::value;
         return log_group == 5   ? launch_group<T, 0, kGated>(p, s)

@@ -227,11 +227,15 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
     skinny::wave_steps(nsteps, NW, wave, s0, s1);
 
     // rows past M re-read the last one; their sums are not stored
+    auto row_x = [&](int rb) {
+        return p.X + (int64_t)(mbase + min(16 * rb + i, rows_x - 1)) * p.ldx;
+    };
+    // k of the row's last whole piece; where it has none, the weight's first bytes are loaded
+    const int whole = p.K & ~7, klast = max(whole - 8, 0);
     const uint16_t* xrow[RB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
-        xrow[rb] = p.X + (int64_t)(mbase + min(16 * rb + i, rows_x - 1)) * p.ldx;
-    const int whole = p.K & ~7;
+        xrow[rb] = whole > 0 ? row_x(rb) : reinterpret_cast<const uint16_t*>(p.W[0]);
 
     floatx4 acc[RB][CB];
 #pragma unroll
@@ -280,34 +284,20 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
     // row ends in it the last ones of the row.
     auto group_at = [&](int s) DGT_INLINE { return min(GPS * s, p.groups - G::kRun); };
     // Activations of step s (past the last step: the last one's): RB*P vector
-    // loads, which the waits below count on.  What lies past K is loaded from the weight's first
-    // bytes and replaced in `prepare`.
+    // loads, which the waits below count on.  Past K the row's last whole piece is loaded, and
+    // replaced in `prepare`.  (No branch: where two ways meet, the compiler counts the
+    // loads of the shorter one and waits for copies that are still on their way.)
     auto load_ops = [&](int s, Ops& o) DGT_INLINE {
         s = min(s, nsteps - 1);
         const int k0 = G::KS * s + 8 * GB * g;
-        if (G::KS * (s + 1) <= p.K) {  // uniform
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const uint16_t* from = xrow[rb] + k0;
+        for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from + piece(e));
-                    o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
-                }
+            for (int e = 0; e < P; ++e) {
+                const u32x4_any v =
+                    *reinterpret_cast<const u32x4_any*>(xrow[rb] + min(k0 + piece(e), klast));
+                o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
             }
-        } else {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    const int k = k0 + piece(e);
-                    const void* from = k < whole ? static_cast<const void*>(xrow[rb] + k)
-                                                 : static_cast<const void*>(p.W[0]);
-                    const u32x4_any v = *static_cast<const u32x4_any*>(from);
-                    o.a[rb][e] = u32x4{v[0], v[1], v[2], v[3]};
-                    asm volatile("" ::: "memory");  // one address at a time
-                }
-        }
     };
     // The run of scales and zero points from step s on (none of the row's where
     // there are fewer or no zero points: then replaced in `prepare`).
@@ -382,7 +372,7 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
             for (int rb = 0; rb < RB; ++rb) {
                 u32x4 tail = {0u, 0u, 0u, 0u};  // the row's last elements, fewer than 8
                 if (kW4 && whole < p.K)
-                    tail = skinny::load16_cached<uint16_t, true, true>(xrow[rb], whole, p.K, true);
+                    tail = skinny::load16_cached<uint16_t, true, true>(row_x(rb), whole, p.K, true);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     const int k = G::KS * s + 8 * GB * g + piece(e);
@@ -663,4 +653,11 @@ hipError_t launch(const Params& p, hipStream_t s) {
 }
 
 }  // namespace strip
+
+namespace w4 {
+// The kernel with shared activations (k_w4_rows.hip) and the operands it takes.
+bool rows_eligible(const strip::Params& p);
+hipError_t launch_rows(In t, bool gate, int log_group, const strip::Params& p, hipStream_t s);
+}  // namespace w4
+
 }  // namespace dgt
