@@ -1,10 +1,10 @@
 // k_gated_regs.hip -- the gated projections and their gradient for operands of
 // any alignment, staged through registers.
 //
-// Tile 128 rows by 128 products, 2 x 2 wavefronts of 64 x 64 (2 x 2
-// v_mfma_f32_32x32x16).  Forward: a wavefront's 64 products are 32 of the gate and
+// Tile BM rows by BB products, 2 x 2 wavefronts of BM/2 x BB/2 (v_mfma_f32_32x32x16).
+// Forward: a wavefront's 64 products are 32 of the gate and
 // the same 32 columns of the other projection, so that both pre-activations of
-// an element end up in one lane.  Gradient: 64 columns of dh.
+// an element end up in one lane.  Gradient: BB columns of dh.
 //
 // K advances in slices of 64, the next one loaded into registers while the
 // current one is multiplied from LDS (two buffers, one barrier a slice).  A
@@ -13,6 +13,7 @@
 // re-reading the last one (their products are not stored); the last, partial slice
 // and column blocks that cross N are gathered element by element with zeros outside.
 // Chunk q (8 k) of row r sits at q ^ ((r ^ r>>3) & 7).
+#include "dma_common.hpp"
 #include "gated.hpp"
 
 namespace dgt {
@@ -20,7 +21,7 @@ namespace gated {
 
 namespace {
 
-constexpr int BM = 128, BB = 128, BK = 64, NT = 256, CPR = BK / 8;
+constexpr int BK = 64, NT = 256, CPR = BK / 8;
 
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
 
@@ -46,58 +47,63 @@ __device__ __forceinline__ u32x4 gather8(const uint16_t* row, int at, int limit)
     return v;
 }
 
-// An operand stored with k contiguous: lane chunk i is staged row tid/8 + 32*i,
+// An operand stored with k contiguous, R rows of it: lane chunk i is staged row tid/8 + 32*i,
 // chunk tid%8.
+template <int R>
 struct Rows {
-    const uint16_t* row[4];
-    u32x4 v[4];
+    static constexpr int C = R / 32;
+    const uint16_t* row[C];
+    u32x4 v[C];
     __device__ void load(int k0, int K, int q) {
         const int at = k0 + 8 * q;
         if (k0 + BK <= K) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = load16(row[i] + at);
+            for (int i = 0; i < C; ++i) v[i] = load16(row[i] + at);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = gather8(row[i], at, K);
+            for (int i = 0; i < C; ++i) v[i] = gather8(row[i], at, K);
         }
     }
     __device__ void store(u32x4* dst, int tid) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < C; ++i) {
             const int r = (tid >> 3) + 32 * i;
             dst[r * CPR + ((tid & 7) ^ swz(r))] = v[i];
         }
     }
 };
 
-// An operand stored K x N: the lane takes k-rows 4*(tid/16) .. +3, columns
-// 8*(tid%16) .. +7 of the tile, and writes them as eight columns of 4 k.
+// An operand stored K x N, BB columns of it: the lane takes KR k-rows from KR*(tid/G) on,
+// columns 8*(tid%G) .. +7 of the tile, and writes them as eight columns of KR k.
+template <int BB>
 struct Columns {
-    u32x4 v[4];
+    static constexpr int G = BB / 8, KR = BK * G / NT;
+    static_assert(KR == 2 || KR == 4, "whole dwords, inside a chunk");
+    u32x4 v[KR];
     __device__ void load(const uint16_t* W, int64_t ld, int n0, int N, int k0, int K, int tid) {
-        const int col = n0 + 8 * (tid & 15), k = k0 + 4 * (tid >> 4);
+        const int col = n0 + 8 * (tid % G), k = k0 + KR * (tid / G);
         if (k0 + BK <= K && n0 + BB <= N) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = load16(W + (int64_t)(k + i) * ld + col);
+            for (int i = 0; i < KR; ++i) v[i] = load16(W + (int64_t)(k + i) * ld + col);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < KR; ++i)
                 v[i] = gather8(W + (int64_t)min(k + i, K - 1) * ld, col, k + i < K ? N : 0);
         }
     }
     __device__ void store(u32x4* dst, int tid) const {
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        const int k = 4 * (tid >> 4);
+        const int k = KR * (tid / G);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int n = 8 * (tid & 15) + j;
-            u32x2 c;
+            const int n = 8 * (tid % G) + j;
+            uint32_t c[KR / 2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < KR / 2; ++e) {
                 const uint32_t a = v[2 * e][j / 2], b = v[2 * e + 1][j / 2];
                 c[e] = j % 2 ? (a >> 16) | (b & 0xffff0000u) : (a & 0xffffu) | (b << 16);
             }
-            *(reinterpret_cast<u32x2*>(dst + n * CPR + ((k / 8) ^ swz(n))) + (k / 4) % 2) = c;
+            uint32_t* to = reinterpret_cast<uint32_t*>(dst + n * CPR + ((k / 8) ^ swz(n))) + k % 8 / 2;
+            __builtin_memcpy(__builtin_assume_aligned(to, 2 * KR), c, 2 * KR);
         }
     }
 };
@@ -107,14 +113,14 @@ struct Place {
 };
 
 // The sums of one tile; load and store move slice k0 of both operands.
-template <In T, typename Load, typename Store>
+template <In T, int BM, int BB, typename Load, typename Store>
 __device__ __forceinline__ void products(int K, const u32x4 (*As)[BM * CPR],
                                          const u32x4 (*Bs)[BB * CPR], const Place& at, Load&& load,
-                                         Store&& store, floatx16 (&acc)[2][2]) {
+                                         Store&& store, floatx16 (&acc)[BM / 64][BB / 64]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < BM / 64; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < BB / 64; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const int nk = K / BK + (K % BK != 0);
@@ -128,17 +134,21 @@ __device__ __forceinline__ void products(int K, const u32x4 (*As)[BM * CPR],
 #pragma unroll
         for (int s = 0; s < BK / 16; ++s) {
             const int q = 2 * s + at.h;
-            u32x4 a[2], b[2];
+            u32x4 a[BM / 64], b[BB / 64];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int ra = at.wm * 64 + i * 32 + at.c, rb = at.wn * 64 + i * 32 + at.c;
-                a[i] = As[buf][ra * CPR + (q ^ swz(ra))];
-                b[i] = Bs[buf][rb * CPR + (q ^ swz(rb))];
+            for (int i = 0; i < BM / 64; ++i) {
+                const int r = at.wm * (BM / 2) + i * 32 + at.c;
+                a[i] = As[buf][r * CPR + (q ^ swz(r))];
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < BB / 64; ++j) {
+                const int r = at.wn * (BB / 2) + j * 32 + at.c;
+                b[j] = Bs[buf][r * CPR + (q ^ swz(r))];
+            }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16<T>(a[i], b[j], acc[i][j]);
+            for (int i = 0; i < BM / 64; ++i)
+#pragma unroll
+                for (int j = 0; j < BB / 64; ++j) acc[i][j] = mfma32x32x16<T>(a[i], b[j], acc[i][j]);
         }
         if (t + 1 < nk) store(buf ^ 1);
         __syncthreads();
@@ -153,23 +163,27 @@ __device__ __forceinline__ Place place() {
 // Row of register r of an MFMA tile (32x32 accumulator layout).
 __device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
-template <In T>
+template <In T, int BM>
 __global__ __launch_bounds__(NT, 2) void forward_regs_kernel(Forward p, int tiles_n) {
+    constexpr int BB = 128;
     __shared__ u32x4 As[2][BM * CPR], Bs[2][BB * CPR];
     const int tid = threadIdx.x;
     const Place at = place();
     const int m0 = (int)(blockIdx.x / (unsigned)tiles_n) * BM;
     const int n0 = (int)(blockIdx.x % (unsigned)tiles_n) * (BB / 2);
-    Rows ra, rb;
+    Rows<BM> ra;
+    Rows<BB> rb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < BM / 32; ++i)
+        ra.row[i] = p.X + (int64_t)min(m0 + (tid >> 3) + 32 * i, p.M - 1) * p.ldx;
+#pragma unroll
+    for (int i = 0; i < BB / 32; ++i) {
         const int r = (tid >> 3) + 32 * i;
-        ra.row[i] = p.X + (int64_t)min(m0 + r, p.M - 1) * p.ldx;
         const int64_t n = min(n0 + 32 * (r / 64) + r % 32, p.N - 1);
         rb.row[i] = (r / 32) % 2 ? p.Wu + n * p.ldwu : p.Wg + n * p.ldwg;
     }
-    floatx16 acc[2][2];
-    products<T>(
+    floatx16 acc[BM / 64][BB / 64];
+    products<T, BM, BB>(
         p.K, As, Bs, at,
         [&](int k0) {
             ra.load(k0, p.K, tid & 7);
@@ -184,10 +198,10 @@ __global__ __launch_bounds__(NT, 2) void forward_regs_kernel(Forward p, int tile
     if (col >= p.N) return;
     const float bg = p.bg ? p.bg[col] : 0.0f, bu = p.bu ? p.bu[col] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < BM / 64; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int64_t row = m0 + 64 * at.wm + 32 * i + acc_row(r, at.h);
+            const int64_t row = m0 + BM / 2 * at.wm + 32 * i + acc_row(r, at.h);
             if (row >= p.M) continue;
             const float g = acc[i][0][r] + bg, u = acc[i][1][r] + bu;
             p.H[row * p.ldh + col] = to_bits<T>(act_of(p.act, g) * u);
@@ -196,20 +210,20 @@ __global__ __launch_bounds__(NT, 2) void forward_regs_kernel(Forward p, int tile
         }
 }
 
-template <In T>
+template <In T, int BM, int BB>
 __global__ __launch_bounds__(NT, 2) void grad_regs_kernel(Grad p, int tiles_n) {
     __shared__ u32x4 As[2][BM * CPR], Bs[2][BB * CPR];
     const int tid = threadIdx.x;
     const Place at = place();
     const int bm = (int)(blockIdx.x / (unsigned)tiles_n);
     const int m0 = bm * BM, n0 = (int)(blockIdx.x % (unsigned)tiles_n) * BB;
-    Rows ra;
-    Columns rb;
+    Rows<BM> ra;
+    Columns<BB> rb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < BM / 32; ++i)
         ra.row[i] = p.dY + (int64_t)min(m0 + (tid >> 3) + 32 * i, p.M - 1) * p.lddy;
-    floatx16 acc[2][2];
-    products<T>(
+    floatx16 acc[BM / 64][BB / 64];
+    products<T, BM, BB>(
         p.K, As, Bs, at,
         [&](int k0) {
             ra.load(k0, p.K, tid & 7);
@@ -221,31 +235,57 @@ __global__ __launch_bounds__(NT, 2) void grad_regs_kernel(Grad p, int tiles_n) {
         },
         acc);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int col = n0 + 64 * at.wn + 32 * j + at.c;
+    for (int j = 0; j < BB / 64; ++j) {
+        const int col = n0 + BB / 2 * at.wn + 32 * j + at.c;
+        const int64_t from = min(col, p.N - 1);
         float sg = 0.0f, su = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < BM / 64; ++i) {
+            // R rows' loads first, those past the edges from the last row or column: behind a
+            // branch each would wait for one another
+            constexpr int R = 8;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t row = m0 + 64 * at.wm + 32 * i + acc_row(r, at.h);
-                if (row >= p.M || col >= p.N) continue;
-                const GradOut o = grad_at(p.act, acc[i][j][r], InFmt<T>::widen(p.G[row * p.ldg + col]),
-                                          InFmt<T>::widen(p.U[row * p.ldu + col]));
-                p.dG[row * p.lddg + col] = to_bits<T>(o.dg);
-                p.dU[row * p.lddu + col] = to_bits<T>(o.du);
-                if (p.H) p.H[row * p.ldh + col] = to_bits<T>(o.h);
-                sg += o.dg;
-                su += o.du;
+            for (int r0 = 0; r0 < 16; r0 += R) {
+                // opaque: the addresses of all rows made ahead would not fit the registers
+                int row0 = m0 + BM / 2 * at.wm + 32 * i;
+                asm volatile("" : "+v"(row0));
+                uint16_t g[R], u[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int64_t row = min(row0 + acc_row(r0 + r, at.h), p.M - 1);
+                    g[r] = p.G[row * p.ldg + from];
+                    u[r] = p.U[row * p.ldu + from];
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int64_t row = row0 + acc_row(r0 + r, at.h);
+                    const GradOut o = grad_at(p.act, acc[i][j][r0 + r], InFmt<T>::widen(g[r]),
+                                              InFmt<T>::widen(u[r]));
+                    if (row >= p.M || col >= p.N) continue;
+                    p.dG[row * p.lddg + col] = to_bits<T>(o.dg);
+                    p.dU[row * p.lddu + col] = to_bits<T>(o.du);
+                    if (p.H) p.H[row * p.ldh + col] = to_bits<T>(o.h);
+                    sg += o.dg;
+                    su += o.du;
+                }
             }
-        if (p.parts) {
-            sg += __shfl_xor(sg, 32);
-            su += __shfl_xor(su, 32);
-            float* part = p.parts + 2 * (int64_t)(2 * bm + at.wm) * p.N;
-            if (at.h == 0 && col < p.N) {
-                part[col] = sg;
-                part[p.N + col] = su;
-            }
+        }
+        if (!p.parts) continue;  // uniform
+        // a part is kPartRows rows: a wavefront's, or two wavefronts' joined in LDS
+        sg += __shfl_xor(sg, 32);
+        su += __shfl_xor(su, 32);
+        constexpr bool kJoin = BM / 2 < kPartRows;
+        float* half = reinterpret_cast<float*>(As[0]) + 2 * (BB / 2 * at.wn + 32 * j + at.c);
+        if (kJoin) {
+            if (at.wm == 1 && at.h == 0) half[0] = sg, half[1] = su;
+            __syncthreads();
+            if (at.wm == 0) sg += half[0], su += half[1];
+        }
+        const int64_t at_part = kJoin ? bm : 2 * (int64_t)bm + at.wm;
+        if (at.h == 0 && col < p.N && (!kJoin || at.wm == 0)) {
+            float* part = p.parts + 2 * at_part * p.N;
+            part[col] = sg;
+            part[p.N + col] = su;
         }
     }
 }
@@ -275,24 +315,38 @@ bool launchable(int64_t wgs) { return wgs < (int64_t(1) << 32) / NT; }
 
 }  // namespace
 
-template <In T>
-hipError_t launch_forward_regs(const Forward& p, hipStream_t s) {
-    const int64_t tiles_n = ((int64_t)p.N + BB / 2 - 1) / (BB / 2);
+// Tiles of 64 rows (gradient: 64 x 64) where those of 128 would leave CUs without one.
+template <In T, int BM>
+hipError_t launch_forward_rows(const Forward& p, hipStream_t s) {
+    const int64_t tiles_n = ((int64_t)p.N + 63) / 64;
     const int64_t wgs = tiles_n * (((int64_t)p.M + BM - 1) / BM);
+    if (BM == 128 && wgs < dma::kCUs) return launch_forward_rows<T, 64>(p, s);
     if (!launchable(wgs)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(forward_regs_kernel<T>, dim3((unsigned)wgs), dim3(NT), 0, s, p,
+    hipLaunchKernelGGL((forward_regs_kernel<T, BM>), dim3((unsigned)wgs), dim3(NT), 0, s, p,
+                       (int)tiles_n);
+    return hipGetLastError();
+}
+
+template <In T, int B>
+hipError_t launch_grad_rows(const Grad& p, int64_t* parts, hipStream_t s) {
+    const int64_t tiles_n = ((int64_t)p.N + B - 1) / B, tiles_m = ((int64_t)p.M + B - 1) / B;
+    const int64_t wgs = tiles_n * tiles_m;
+    if (B == 128 && wgs < dma::kCUs) return launch_grad_rows<T, 64>(p, parts, s);
+    if (!launchable(wgs)) return hipErrorInvalidConfiguration;
+    *parts = B / kPartRows * tiles_m;
+    hipLaunchKernelGGL((grad_regs_kernel<T, B, B>), dim3((unsigned)wgs), dim3(NT), 0, s, p,
                        (int)tiles_n);
     return hipGetLastError();
 }
 
 template <In T>
+hipError_t launch_forward_regs(const Forward& p, hipStream_t s) {
+    return launch_forward_rows<T, 128>(p, s);
+}
+
+template <In T>
 hipError_t launch_grad_regs(const Grad& p, int64_t* parts, hipStream_t s) {
-    const int64_t tiles_n = ((int64_t)p.N + BB - 1) / BB;
-    const int64_t wgs = tiles_n * (((int64_t)p.M + BM - 1) / BM);
-    if (!launchable(wgs)) return hipErrorInvalidConfiguration;
-    *parts = parts_for(p.M, BM);
-    hipLaunchKernelGGL(grad_regs_kernel<T>, dim3((unsigned)wgs), dim3(NT), 0, s, p, (int)tiles_n);
-    return hipGetLastError();
+    return launch_grad_rows<T, 128>(p, parts, s);
 }
 
 hipError_t launch_join(const float* parts, int64_t n_parts, int N, float* dbg, float* dbu,
