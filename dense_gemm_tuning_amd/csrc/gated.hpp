@@ -43,6 +43,42 @@ struct Grad {
 constexpr int kPartRows = 64;
 inline int64_t parts_for(int M, int tile) { return 2 * (((int64_t)M + tile - 1) / tile); }
 
+// 16 bytes from wherever they start.
+__device__ __forceinline__ u32x4 load16(const uint16_t* from) {
+    u32x4 v;
+    __builtin_memcpy(&v, from, 16);
+    return v;
+}
+
+// Elements [at, at + 8) of a row of fewer than 8, zeros behind it (limit >= 1).
+__device__ __forceinline__ u32x4 gather8(const uint16_t* row, int at, int limit) {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = row[min(at + i, limit - 1)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = at + i < limit ? e[i] : 0u;
+    return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+}
+
+// The 8 elements from `past` (0 .. 8) on, zeros behind them.  A piece that crosses a row's end is
+// the row's last 8 elements so shifted: its load needs no branch, behind which it would wait
+// for the others.
+__device__ __forceinline__ u32x4 shift_out(u32x4 v, int past) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        if (past & 1) v[d] = (v[d] >> 16) | (d < 3 ? v[(d + 1) % 4] << 16 : 0u);
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        if (past & 2) v[d] = d < 3 ? v[(d + 1) % 4] : 0u;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        if (past & 4) v[d] = d < 2 ? v[(d + 2) % 4] : 0u;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        if (past & 8) v[d] = 0u;
+    return v;
+}
+
 // t = exp(-|x|) and the logistic function of x and of -x from it: no
 // cancellation on either side.  The reciprocal is the hardware's, to 1 ulp like
 // exp2, and the argument's rounding adds |x| * 2^-24: what is computed from

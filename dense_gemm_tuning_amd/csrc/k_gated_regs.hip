@@ -7,11 +7,9 @@
 // an element end up in one lane.  Gradient: BB columns of dh.
 //
 // K advances in slices of 64, the next one loaded into registers while the
-// current one is multiplied from LDS (two buffers, one barrier a slice).  A
-// slice that lies inside K is loaded 16 bytes at a time from wherever a row
-// starts (the GPU runs with unaligned access enabled), rows past the end
-// re-reading the last one (their products are not stored); the last, partial slice
-// and column blocks that cross N are gathered element by element with zeros outside.
+// current one is multiplied from LDS (two buffers, one barrier a slice), 16 bytes at a time
+// from wherever a row starts (the GPU runs with unaligned access enabled), rows past the
+// end re-reading the last one (their products are not stored).
 // Chunk q (8 k) of row r sits at q ^ ((r ^ r>>3) & 7).
 #include "dma_common.hpp"
 #include "gated.hpp"
@@ -25,26 +23,11 @@ constexpr int BK = 64, NT = 256, CPR = BK / 8;
 
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
 
-__device__ __forceinline__ u32x4 load16(const uint16_t* src) {
-    u32x4 v;
-    __builtin_memcpy(&v, src, 16);
-    return v;
-}
-
-// Elements [at, at + 8) of a row, zeros from `limit` on.  Every element is loaded, those past the
-// row's end from its last one: loads behind a branch each would wait for one another.
-__device__ __forceinline__ u32x4 gather8(const uint16_t* row, int at, int limit) {
-    uint32_t e[8];
-#pragma unroll
-    for (int d = 0; d < 8; ++d) e[d] = row[max(min(at + d, limit - 1), 0)];
-    u32x4 v;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint32_t lo = at + 2 * d < limit ? e[2 * d] : 0u;
-        const uint32_t hi = at + 2 * d + 1 < limit ? e[2 * d + 1] : 0u;
-        v[d] = lo | (hi << 16);
-    }
-    return v;
+// In the loads below a whole 16 bytes lies inside the row: those of a piece that crosses its end
+// or lies behind it are the row's last ones, put right where they are stored to LDS (a load's
+// value used before the products would be waited for there).  Rows of fewer than 8 are gathered.
+__device__ __forceinline__ int past_end(int at, int limit) {
+    return limit >= 8 ? min(max(at - (limit - 8), 0), 8) : 0;
 }
 
 // An operand stored with k contiguous, R rows of it: lane chunk i is staged row tid/8 + 32*i,
@@ -54,45 +37,59 @@ struct Rows {
     static constexpr int C = R / 32;
     const uint16_t* row[C];
     u32x4 v[C];
-    __device__ void load(int k0, int K, int q) {
-        const int at = k0 + 8 * q;
-        if (k0 + BK <= K) {
-#pragma unroll
-            for (int i = 0; i < C; ++i) v[i] = load16(row[i] + at);
-        } else {
+    int at, K;
+    template <bool kFirst>
+    __device__ void load(std::bool_constant<kFirst>, int k0, int K_, int q) {
+        at = k0 + 8 * q;
+        K = K_;
+        if (kFirst && K < 8) {  // uniform; then there is one slice
 #pragma unroll
             for (int i = 0; i < C; ++i) v[i] = gather8(row[i], at, K);
+            return;
         }
+        const int from = min(at, K - 8);
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = load16(row[i] + from);
     }
     __device__ void store(u32x4* dst, int tid) const {
+        const bool cut = at - 8 * (tid & 7) + BK > K;  // uniform
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int r = (tid >> 3) + 32 * i;
-            dst[r * CPR + ((tid & 7) ^ swz(r))] = v[i];
+            dst[r * CPR + ((tid & 7) ^ swz(r))] = cut ? shift_out(v[i], past_end(at, K)) : v[i];
         }
     }
 };
 
 // An operand stored K x N, BB columns of it: the lane takes KR k-rows from KR*(tid/G) on,
-// columns 8*(tid%G) .. +7 of the tile, and writes them as eight columns of KR k.
-template <int BB>
+// columns 8*(tid%G) .. +7 of the tile, and writes them as eight columns of KR k.  kNarrow: N < 8.
+template <int BB, bool kNarrow>
 struct Columns {
     static constexpr int G = BB / 8, KR = BK * G / NT;
     static_assert(KR == 2 || KR == 4, "whole dwords, inside a chunk");
     u32x4 v[KR];
-    __device__ void load(const uint16_t* W, int64_t ld, int n0, int N, int k0, int K, int tid) {
-        const int col = n0 + 8 * (tid % G), k = k0 + KR * (tid / G);
-        if (k0 + BK <= K && n0 + BB <= N) {
+    int col, N, k, K;
+    bool cut;  // the slice or the tile crosses an end (uniform)
+    __device__ void load(const uint16_t* W, int64_t ld, int n0, int N_, int k0, int K_, int tid) {
+        N = N_;
+        K = K_;
+        col = n0 + 8 * (tid % G);
+        k = k0 + KR * (tid / G);
+        cut = k0 + BK > K || n0 + BB > N;
 #pragma unroll
-            for (int i = 0; i < KR; ++i) v[i] = load16(W + (int64_t)(k + i) * ld + col);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KR; ++i)
-                v[i] = gather8(W + (int64_t)min(k + i, K - 1) * ld, col, k + i < K ? N : 0);
+        for (int i = 0; i < KR; ++i) {
+            const uint16_t* row = W + (int64_t)min(k + i, K - 1) * ld;
+            if (kNarrow) v[i] = gather8(row, col, N);
+            else v[i] = load16(row + min(col, N - 8));
         }
     }
-    __device__ void store(u32x4* dst, int tid) const {
-        const int k = KR * (tid / G);
+    __device__ void store(u32x4* dst, int tid) {
+        const int kk = KR * (tid / G);
+        if (cut) {
+            const int past = past_end(col, N);
+#pragma unroll
+            for (int i = 0; i < KR; ++i) v[i] = shift_out(v[i], k + i < K ? past : 8);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int n = 8 * (tid % G) + j;
@@ -102,7 +99,8 @@ struct Columns {
                 const uint32_t a = v[2 * e][j / 2], b = v[2 * e + 1][j / 2];
                 c[e] = j % 2 ? (a >> 16) | (b & 0xffff0000u) : (a & 0xffffu) | (b << 16);
             }
-            uint32_t* to = reinterpret_cast<uint32_t*>(dst + n * CPR + ((k / 8) ^ swz(n))) + k % 8 / 2;
+            uint32_t* to =
+                reinterpret_cast<uint32_t*>(dst + n * CPR + ((kk / 8) ^ swz(n))) + kk % 8 / 2;
             __builtin_memcpy(__builtin_assume_aligned(to, 2 * KR), c, 2 * KR);
         }
     }
@@ -125,12 +123,12 @@ __device__ __forceinline__ void products(int K, const u32x4 (*As)[BM * CPR],
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const int nk = K / BK + (K % BK != 0);
     if (nk == 0) return;
-    load(0);
+    load(std::true_type{}, 0);
     store(0);
     __syncthreads();
     for (int t = 0; t < nk; ++t) {
         const int buf = t & 1;
-        if (t + 1 < nk) load((t + 1) * BK);
+        if (t + 1 < nk) load(std::false_type{}, (t + 1) * BK);
 #pragma unroll
         for (int s = 0; s < BK / 16; ++s) {
             const int q = 2 * s + at.h;
@@ -185,9 +183,9 @@ __global__ __launch_bounds__(NT, 2) void forward_regs_kernel(Forward p, int tile
     floatx16 acc[BM / 64][BB / 64];
     products<T, BM, BB>(
         p.K, As, Bs, at,
-        [&](int k0) {
-            ra.load(k0, p.K, tid & 7);
-            rb.load(k0, p.K, tid & 7);
+        [&](auto first, int k0) {
+            ra.load(first, k0, p.K, tid & 7);
+            rb.load(first, k0, p.K, tid & 7);
         },
         [&](int buf) {
             ra.store(As[buf], tid);
@@ -210,7 +208,7 @@ __global__ __launch_bounds__(NT, 2) void forward_regs_kernel(Forward p, int tile
         }
 }
 
-template <In T, int BM, int BB>
+template <In T, int BM, int BB, bool kNarrow>
 __global__ __launch_bounds__(NT, 2) void grad_regs_kernel(Grad p, int tiles_n) {
     __shared__ u32x4 As[2][BM * CPR], Bs[2][BB * CPR];
     const int tid = threadIdx.x;
@@ -218,15 +216,15 @@ __global__ __launch_bounds__(NT, 2) void grad_regs_kernel(Grad p, int tiles_n) {
     const int bm = (int)(blockIdx.x / (unsigned)tiles_n);
     const int m0 = bm * BM, n0 = (int)(blockIdx.x % (unsigned)tiles_n) * BB;
     Rows<BM> ra;
-    Columns<BB> rb;
+    Columns<BB, kNarrow> rb;
 #pragma unroll
     for (int i = 0; i < BM / 32; ++i)
         ra.row[i] = p.dY + (int64_t)min(m0 + (tid >> 3) + 32 * i, p.M - 1) * p.lddy;
     floatx16 acc[BM / 64][BB / 64];
     products<T, BM, BB>(
         p.K, As, Bs, at,
-        [&](int k0) {
-            ra.load(k0, p.K, tid & 7);
+        [&](auto first, int k0) {
+            ra.load(first, k0, p.K, tid & 7);
             rb.load(p.Wd, p.ldw, n0, p.N, k0, p.K, tid);
         },
         [&](int buf) {
@@ -334,9 +332,11 @@ hipError_t launch_grad_rows(const Grad& p, int64_t* parts, hipStream_t s) {
     if (B == 128 && wgs < dma::kCUs) return launch_grad_rows<T, 64>(p, parts, s);
     if (!launchable(wgs)) return hipErrorInvalidConfiguration;
     *parts = B / kPartRows * tiles_m;
-    hipLaunchKernelGGL((grad_regs_kernel<T, B, B>), dim3((unsigned)wgs), dim3(NT), 0, s, p,
-                       (int)tiles_n);
-    return hipGetLastError();
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, s, p, (int)tiles_n);
+        return hipGetLastError();
+    };
+    return p.N < 8 ? go(grad_regs_kernel<T, B, B, true>) : go(grad_regs_kernel<T, B, B, false>);
 }
 
 template <In T>

@@ -24,21 +24,6 @@ using namespace mfma16;
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // Eight 16-bit values at columns col .. col+7 of a row of N, at any alignment.
-template <bool kEdge>
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, int col, int N) {
-    if (!kEdge || col + 8 <= N) {
-        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(row + col);
-        return u32x4{v[0], v[1], v[2], v[3]};
-    }
-    u32x4 v;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint32_t lo = col + 2 * d < N ? row[col + 2 * d] : 0u;
-        const uint32_t hi = col + 2 * d + 1 < N ? row[col + 2 * d + 1] : 0u;
-        v[d] = lo | (hi << 16);
-    }
-    return v;
-}
 template <In T, bool kEdge>
 __device__ __forceinline__ void store8(uint16_t* row, int col, int N, const float (&x)[8]) {
     uint16_t b[8];
@@ -132,17 +117,18 @@ __global__ __launch_bounds__(NT, R == 256 ? 1 : 2) void forward_tile_kernel(Gemm
 }
 
 // The gradient's epilogue of one wavefront, its rows from row0 and columns from
-// colw on.  kEdge: rows or columns may lie past the end; these tiles load a piece (8
-// columns of a row) where they use it, whole ones B pieces ahead: 8 KB in flight a
-// wavefront at 256 x 256, 4 at 128 x 128, where there are twice the wavefronts.
+// colw on.  kEdge: rows or columns may lie past the end.  Pieces (8 columns of a row) are
+// loaded B ahead: 8 KB in flight a wavefront at 256 x 256, 4 at 128 x 128, where there are twice
+// the wavefronts (at an edge 4 at either: more goes to scratch memory).
 template <In T, int R, bool kEdge>
 __device__ __forceinline__ void grad_epilogue(const Grad& p, const floatx16 (&acc)[Geo<R>::TM][Geo<R>::TM],
                                               int row0, int colw, int part, int lane, uint8_t* mem) {
     using Ch = Chunk<R>;
     const Ch chunk{reinterpret_cast<float*>(mem)};
-    constexpr int B = kEdge ? 1 : R / 64, BATCHES = Ch::PIECES / B, ALL = Geo<R>::TM * BATCHES;
+    constexpr int B = kEdge ? 2 : R / 64, BATCHES = Ch::PIECES / B, ALL = Geo<R>::TM * BATCHES;
     static_assert(Ch::PIECES % B == 0 && 64 % Ch::GROUPS == 0, "a lane's columns are one group's");
     const int c = Ch::col(0, lane), col = colw + c;
+    const int past = kEdge && p.N >= 8 ? min(max(col - (p.N - 8), 0), 8) : 0;
     u32x4 vg[B], vu[B];
     float sg[8], su[8];
 #pragma unroll
@@ -155,21 +141,28 @@ __device__ __forceinline__ void grad_epilogue(const Grad& p, const floatx16 (&ac
         for (int i = 0; i < B; ++i) {
             // rows past the end re-read the last one
             const int64_t row = kEdge ? min(row0 + row_of(b, i), p.M - 1) : row0 + row_of(b, i);
-            vg[i] = load8<kEdge>(p.G + row * p.ldg, col, p.N);
-            vu[i] = load8<kEdge>(p.U + row * p.ldu, col, p.N);
+            const uint16_t *g = p.G + row * p.ldg, *u = p.U + row * p.ldu;
+            if (kEdge && p.N < 8) {  // uniform
+                vg[i] = gather8(g, col, p.N);
+                vu[i] = gather8(u, col, p.N);
+            } else {  // what crosses a row's end is shifted where it is used
+                const int from = kEdge ? min(col, p.N - 8) : col;
+                vg[i] = load16(g + from);
+                vu[i] = load16(u + from);
+            }
         }
     };
     with_act(p.act, [&](auto a) DGT_INLINE {
-        if constexpr (!kEdge) fetch(0);
+        fetch(0);
 #pragma unroll 1
         for (int b = 0; b < ALL; ++b) {
-            if constexpr (kEdge) fetch(b);
             u32x4 cg[B], cu[B];
 #pragma unroll
-            for (int i = 0; i < B; ++i) cg[i] = vg[i], cu[i] = vu[i];
-            if constexpr (!kEdge) {
-                if (b + 1 < ALL) fetch(b + 1);
+            for (int i = 0; i < B; ++i) {
+                cg[i] = kEdge ? shift_out(vg[i], past) : vg[i];
+                cu[i] = kEdge ? shift_out(vu[i], past) : vu[i];
             }
+            if (b + 1 < ALL) fetch(b + 1);
             if (b % BATCHES == 0) put_row<R>(chunk, acc, b / BATCHES, lane);
 #pragma unroll
             for (int i = 0; i < B; ++i) {
