@@ -313,7 +313,11 @@ bool launchable(int64_t wgs) { return wgs < (int64_t(1) << 32) / NT; }
 
 }  // namespace
 
-// Tiles of 64 rows (gradient: 64 x 64) where those of 128 would leave CUs without one.
+// Tiles of 64 rows (gradient: 64 x 64) where those of 128 would leave CUs without one (us, 64
+// against 128, forward and gradient at K = 1001: 16 x 1000 17.7/23.1 and 16.3/35.4, 1000 x 1000
+// 21.6/29.9 and 20.0/40.9, 1500 x 1000 25.9/30.3 and 21.6/41.6).  What bounds them is the
+// loads of rows that start off 16-byte boundaries: 2048 x 8192 x 1001 forward takes 141 us here and
+// 87 on the DMA tiles when its rows are 1008 apart.
 template <In T, int BM>
 hipError_t launch_forward_rows(const Forward& p, hipStream_t s) {
     const int64_t tiles_n = ((int64_t)p.N + 63) / 64;
