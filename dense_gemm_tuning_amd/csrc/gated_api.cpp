@@ -185,7 +185,8 @@ int gemm_gated_grad(int dtype, int act, int M, int N, int K, const uint16_t* dY,
                         rows_of(dY, M, K, lddy, 2), rows_of(Wd, K, N, ldw, 2)};
     for (int o = 0; o < 5; ++o) {
         for (int i = 0; i < 4; ++i)
-            if (share(out[o], in[i]) && !(o == i && same(out[o], in[i]))) return GEMM_ERR_OVERLAP;
+            if (share(out[o], in[i]) && !(i < 2 && o == i && same(out[o], in[i])))  // dG on G, dU on U
+                return GEMM_ERR_OVERLAP;
         for (int q = 0; q < o; ++q)
             if (share(out[o], out[q])) return GEMM_ERR_OVERLAP;
         if (share(out[o], ws)) return GEMM_ERR_OVERLAP;

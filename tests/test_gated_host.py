@@ -64,6 +64,19 @@ def test_grad_argument_checks():
     assert f(dG=G_ + 2) == f(dG=G_, lddg=9) == f(H=G_, ldh=8) == dgt.GEMM_ERR_OVERLAP
 
 
+def test_grad_outputs_over_the_products_operands():
+    need = dgt.gemm_gated_grad_workspace_size(1, 8)
+
+    def f(M=1, N=8, K=8, dY=X_, Wd=A_, H=0, sg=0, su=0):
+        return dgt.gemm_gated_grad(2, 0, M, N, K, dY, K, Wd, N, G_, N, U_, N, D_, N, E_, N, H, N, sg, su,
+                                   W_ if sg or su else 0, need if sg or su else 0)
+
+    # only dG over G and dU over U may share memory: each output stands against every input
+    assert f(H=X_) == f(M=4, H=X_) == f(H=A_) == f(H=U_) == dgt.GEMM_ERR_OVERLAP
+    for k in (1, 8):
+        assert f(K=k, sg=A_) == f(K=k, sg=X_) == f(K=k, sg=G_) == f(K=k, su=A_) == dgt.GEMM_ERR_OVERLAP
+
+
 def _w(group=64, K=100):
     return dict(ldq=64, lds=gp.groups(K, group), ldz=gp.groups(K, group))
 
