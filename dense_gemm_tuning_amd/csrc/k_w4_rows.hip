@@ -17,7 +17,10 @@
 // Workgroups start at different runs and wrap around: all at one k, they would ask for
 // the same columns of rows whose pitch is often a power of two.
 //
-// Bound by the copies of the activations (64 rows: 32 of a step's 48 KB).
+// Bound by the products and the decoding, which share each SIMD's issue and start together behind
+// the barrier: 64 x 28672 x 8192 takes 62 us, 54 without the copies and 35 with them alone (a step's
+// 32 KB of activations and 16 KB of codes); without the sums of x, a third of the products, 52.  (Those
+// sums made once for the four waves that share them, and subtracted a step later, took 65.)
 // 16-byte aligned rows of activations with pitches below 2^24; others take the strips.
 #include <algorithm>
 
@@ -334,6 +337,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
                                  (((p.K / 8 - 4 * CPS * now.k) ^ swz_a(tid)) << 4);
                 for (int e = p.K % 8; e < 8; ++e) reinterpret_cast<uint16_t*>(piece)[e] = 0;
             }
+            fence();
             DMA_WAIT_VMCNT_LGKM0(0);
             dma::barrier();
         }
@@ -351,6 +355,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
             buf ^= 1;
             if (loads_scales) put_scales(next, buf, sc);
         }
+        fence();
         advance(now);
     };
     if (loads_scales) {
@@ -446,7 +451,7 @@ hipError_t launch_group(const Params& p, int log_group, hipStream_t s) {
 }  // namespace
 
 bool rows_eligible(const Params& p) {
-    return rows_16b_aligned(p.X, p.ldx, 2) && p.ldx < kMaxBufferPitch;
+    return p.K > 0 && rows_16b_aligned(p.X, p.ldx, 2) && p.ldx < kMaxBufferPitch;
 }
 
 hipError_t launch_rows(In t, bool gate, int log_group, const Params& p, hipStream_t s) {
