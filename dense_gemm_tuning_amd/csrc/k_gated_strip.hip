@@ -36,6 +36,8 @@ hipError_t launch_forward_strip(const Forward& p, hipStream_t s) {
     q.H = p.H; q.ldh = p.ldh;
     q.G = p.G; q.ldg = p.ldg;
     q.U = p.U; q.ldu = p.ldu;
+    // Strips of 16 outputs where there are few, of 32 and 64 where every CU has them (us, this rule and
+    // strips of 64 alone, K = 8192: 1 x 3584 21 and 30, 16 x 3584 22 and 34, 16 x 8192 55.4 and 57.4).
     if (p.M > 32) return strip::launch<T, Cfg<4, 4, 32, 128>>(q, s);
     if (p.M > 16) return strip::launch<T, Cfg<2, 8, 16, 256>>(q, s);
     if (p.N <= 16 * dma::kCUs) return strip::launch<T, Cfg<1, 2, 16, 256>>(q, s);

@@ -9,7 +9,12 @@ namespace {
 
 using strip::Cfg;
 
-// 2^LG blocks of 32 k a scale group.
+// 2^LG blocks of 32 k a scale group.  Strips of at most as many rows as give every CU one
+// (kGated: half as many outputs), wider ones where there are more rows than that: 16 to 128 rows
+// for up to 16 rows of activations, and up to 128 rows with two blocks of activations for more
+// (which is then only for activations that the shared kernel does not take).  us, with this rule and
+// with strips of 128 rows alone, K = 8192, one row of activations: 3584 9.6 and 20.6, 8192 12.2 and 20.7,
+// 14336 15.6 and 21.4; gated 3584 12.0 and 20.1, 8192 17.4 and 22.6; 16 rows: 3584 14 and 25, 14336 21 and 28.
 template <In T, int LG, bool kGated>
 hipError_t launch_group(const strip::Params& p, hipStream_t s) {
     constexpr int kPair = kGated ? 2 : 1;
@@ -25,6 +30,10 @@ hipError_t launch_group(const strip::Params& p, hipStream_t s) {
 
 template <bool kGated>
 hipError_t launch_strips(In t, int log_group, const strip::Params& p, hipStream_t s) {
+    // Strips load the activations once per strip and wave: more than 16 rows take the kernel that
+    // shares them, where it has work for the CUs.  us, strips against it, K = 8192, group 128: 28672 x 32
+    // 44/43, x 64 80/63, x 256 285/232; 14336 x 32 39/38, x 64 71/55; 8192 x 32 29/37, x 64 51/54, x 128
+    // 92/56; 3584 x 64 43/54, x 128 82/54; gated 8192 x 32 39/39, x 64 69/55; gated 3584 x 64 50/55.
     const bool wide = (kGated ? 2 : 1) * (int64_t)p.N > 32 * dma::kCUs;
     if ((p.M > 64 || (p.M > 16 && wide)) && rows_eligible(p))
         return launch_rows(t, kGated, log_group, p, s);

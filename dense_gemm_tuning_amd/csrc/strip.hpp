@@ -1,6 +1,9 @@
 // strip.hpp -- products of few rows with weights stored N x K (16-bit, or 4-bit
 // with group scales), plain or gated: the kernel of k_gated_strip.hip and
-// k_w4_strip.hip.  The time is the time to stream the weights once.
+// k_w4_strip.hip.  The time is the time to stream the weights once: gated 8 x 28672 x 8192,
+// 140 us for 940 MB of 16-bit weights (6.7 TB/s) and 55 for 241 MB of 4-bit ones (4.4 TB/s); plain
+// 1 x 28672 x 8192 in 4 bits 26 us (4.7 TB/s).  Small weights are bound by the launch and
+// the latency of a wave's steps one after the other (4-bit 1 x 3584 x 8192: 8.7 us for 15 MB).
 //
 // A workgroup owns a strip of outputs over the whole of K, each of its 8
 // waves one range of it; the partial tiles are summed in LDS in wave order
