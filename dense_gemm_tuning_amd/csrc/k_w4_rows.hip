@@ -1,8 +1,8 @@
 // k_w4_rows.hip -- products of more than a few rows with 4-bit weights, plain and
 // gated: what strip.hpp does not reuse, the activations, is shared here.
 //
-// A workgroup has a strip of 128 stored rows of the weight (gated: 64 of the gate's and
-// the same 64 of the other projection's) and up to 16*RBT rows of activations.  A step of 256 k
+// A workgroup has a strip of 64 or 128 stored rows of the weight (gated: half of them of the gate's and
+// the same ones of the other projection's) and 32 or 64 rows of activations.  A step of 256 k
 // of both is copied by DMA into one of three LDS stages, two steps ahead, and one
 // barrier a step both publishes the step and retires the stage before it.  The 8
 // waves split the step's k two ways and the stored rows four ways, each with all
@@ -11,7 +11,7 @@
 //
 // Decoding and the scale groups' sums are strip.hpp's, but that here the codes
 // are put into the activations' order (two byte permutes a dword).  Scales and
-// zero points come in runs of 8 groups: 128 lanes load a row's each in a run's last step and
+// zero points come in runs of 8 groups: a lane for each stored row loads its in a run's last step and
 // write them, joined, to the one of two LDS buffers that the next run reads.
 //
 // Workgroups start at different runs and wrap around: all at one k, they would ask for
@@ -34,12 +34,10 @@ namespace {
 using mx4::static_for;
 using strip::Params;
 
-constexpr int NWAVE = 8, NS = 3, KS = 2, ROWS = 128, ROWB = 128, kRun = 8;
+constexpr int NWAVE = 8, NS = 3, KS = 2, ROWB = 128, kRun = 8;
 constexpr int STEPK = 2 * ROWB, CPS = ROWB / 16;      // k and chunks of a weight's row per step
 constexpr int BPW = STEPK / 32 / KS;                  // blocks of 32 k per wave and step
-constexpr int CBW = ROWS * KS / NWAVE / 16;           // 16-row blocks of the weight per wave
 constexpr int AROW = 2 * STEPK;                       // bytes of a row of activations per step
-constexpr int B_BYTES = ROWS * ROWB, IB = B_BYTES / 1024 / NWAVE;  // copies per wave
 
 using uint32x2 = uint32_t __attribute__((ext_vector_type(2)));
 
@@ -78,43 +76,65 @@ __device__ __forceinline__ u32x4 decode8(uint32_t q) {
 __device__ __forceinline__ uint32_t lds_address(const void* at) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)at;
 }
-// A step's codes of two stored rows 16 apart (four dwords each, at the four addresses) and
+// A step's codes of a stored row, or of two 16 apart (four dwords each, at the four addresses), and
 // the factors of their G groups.  Read by hand: the compiler takes some of the
 // copies on their way for writes of what it reads here, and waits for all of them.
-template <int G>
+template <int G, int CBW>
 __device__ __forceinline__ void read_weight(const uint32_t (&at)[BPW], const uint32_t* factors,
-                                            uint32x2 (&q)[BPW], uint32_t (&f)[CBW][G]) {
-    static_assert(BPW == 4 && CBW == 2 && 16 * kRun * 4 == 512 && 16 * ROWB == 8 * 64 * 4, "the offsets");
+                                            uint32_t (&q)[BPW][CBW], uint32_t (&f)[CBW][G]) {
+    static_assert(BPW == 4 && 16 * kRun * 4 == 512 && 16 * ROWB == 8 * 64 * 4, "the offsets");
+    static_assert((G == 1 || G == 2 || G == 4) && (CBW == 1 || CBW == 2), "a factor's read");
     using V = std::conditional_t<G == 1, uint32_t, std::conditional_t<G == 2, uint32x2, u32x4>>;
-    V v0, v1;
+    V v[2];
     const uint32_t fat = lds_address(factors);
-#define DGT_READ_WEIGHT(F)                                                                  \
-    asm volatile("ds_read2st64_b32 %0, %6 offset1:8\n\t"                                    \
-                 "ds_read2st64_b32 %1, %7 offset1:8\n\t"                                    \
-                 "ds_read2st64_b32 %2, %8 offset1:8\n\t"                                    \
-                 "ds_read2st64_b32 %3, %9 offset1:8\n\t"                                    \
-                 F " %4, %10\n\t"                                                           \
-                 F " %5, %10 offset:512\n\t"                                                \
-                 "s_waitcnt lgkmcnt(0)"                                                     \
-                 : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3]), "=&v"(v0), "=&v"(v1) \
-                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(fat)                 \
+    if constexpr (CBW == 1) {
+#define DGT_READ_WEIGHT(F)                                                                            \
+    asm volatile("ds_read_b32 %0, %5\n\tds_read_b32 %1, %6\n\tds_read_b32 %2, %7\n\tds_read_b32 %3, %8\n\t" \
+                 F " %4, %9\n\ts_waitcnt lgkmcnt(0)"                                                  \
+                 : "=&v"(q[0][0]), "=&v"(q[1][0]), "=&v"(q[2][0]), "=&v"(q[3][0]), "=&v"(v[0])        \
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(fat)                           \
                  : "memory")
-    if constexpr (G == 1) DGT_READ_WEIGHT("ds_read_b32");
-    else if constexpr (G == 2) DGT_READ_WEIGHT("ds_read_b64");
-    else DGT_READ_WEIGHT("ds_read_b128");
+        if constexpr (G == 1) DGT_READ_WEIGHT("ds_read_b32");
+        else if constexpr (G == 2) DGT_READ_WEIGHT("ds_read_b64");
+        else DGT_READ_WEIGHT("ds_read_b128");
 #undef DGT_READ_WEIGHT
-    static_assert(G == 1 || G == 2 || G == 4, "a factor's read");
+    } else {
+        uint32x2 p[BPW];
+#define DGT_READ_WEIGHT(F)                                                                      \
+    asm volatile("ds_read2st64_b32 %0, %6 offset1:8\n\t"                                        \
+                 "ds_read2st64_b32 %1, %7 offset1:8\n\t"                                        \
+                 "ds_read2st64_b32 %2, %8 offset1:8\n\t"                                        \
+                 "ds_read2st64_b32 %3, %9 offset1:8\n\t"                                        \
+                 F " %4, %10\n\t"                                                               \
+                 F " %5, %10 offset:512\n\t"                                                    \
+                 "s_waitcnt lgkmcnt(0)"                                                         \
+                 : "=&v"(p[0]), "=&v"(p[1]), "=&v"(p[2]), "=&v"(p[3]), "=&v"(v[0]), "=&v"(v[1]) \
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(fat)                     \
+                 : "memory")
+        if constexpr (G == 1) DGT_READ_WEIGHT("ds_read_b32");
+        else if constexpr (G == 2) DGT_READ_WEIGHT("ds_read_b64");
+        else DGT_READ_WEIGHT("ds_read_b128");
+#undef DGT_READ_WEIGHT
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-        if constexpr (G == 1) f[0][j] = v0, f[1][j] = v1;
-        else f[0][j] = v0[j], f[1][j] = v1[j];
+        for (int e = 0; e < BPW; ++e)
+#pragma unroll
+            for (int c = 0; c < CBW; ++c) q[e][c] = p[e][c];
     }
+#pragma unroll
+    for (int c = 0; c < CBW; ++c)
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            if constexpr (G == 1) f[c][j] = v[c];
+            else f[c][j] = v[c][j];
+        }
 }
 
-// 2^LG blocks of 32 k a scale group.
-template <In T, int LG, bool kGated, int RBT>
+// 2^LG blocks of 32 k a scale group; RBT blocks of 16 rows of activations, CBW of the weight a wave.
+template <In T, int LG, bool kGated, int RBT, int CBW>
 __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int cols, int mchunks) {
     constexpr int GB = 1 << LG, GPS = STEPK / 32 / GB, GPW = GPS / KS, SPS = kRun / GPS;
+    constexpr int ROWS = 16 * CBW * NWAVE / KS;      // stored rows of a strip
+    constexpr int B_BYTES = ROWS * ROWB, IB = B_BYTES / 1024 / NWAVE;  // copies per wave
     constexpr int kPart = kGated ? ROWS / 2 : ROWS;  // stored rows of one matrix
     constexpr int A_BYTES = 16 * RBT * AROW, IA = A_BYTES / 1024 / NWAVE;
     constexpr int STAGE = B_BYTES + A_BYTES, COPIES = IA + IB;
@@ -271,9 +291,8 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
 #pragma unroll
         for (int e = 0; e < BPW; ++e)
             from[e] = lds_address(st + row0 * ROWB + (((BPW * wk + e) ^ swz_b(row0)) << 4) + 4 * g);
-        uint32x2 q[BPW];
-        uint32_t f[CBW][GPW];
-        read_weight<GPW>(from, factors + (ROWS * buf + row0) * kRun + GPS * at.r + GPW * wk, q, f);
+        uint32_t q[BPW][CBW], f[CBW][GPW];
+        read_weight<GPW, CBW>(from, factors + (ROWS * buf + row0) * kRun + GPS * at.r + GPW * wk, q, f);
 #pragma unroll
         for (int j = 0; j < GPW; ++j) {
             floatx4 sum[RBT][CBW], xs[RBT];
@@ -421,9 +440,9 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
     });
 }
 
-template <In T, int LG, bool kGated, int RBT>
+template <In T, int LG, bool kGated, int RBT, int CBW>
 hipError_t launch(const Params& p, hipStream_t s) {
-    constexpr int most = kGated ? ROWS / 2 : ROWS;
+    constexpr int most = 16 * CBW * NWAVE / KS / (kGated ? 2 : 1);
     const int64_t mchunks = ((int64_t)p.M + 16 * RBT - 1) / (16 * RBT);
     // as narrow as the rounds of the CUs that the widest strips take allow
     const int64_t rounds = (((int64_t)p.N + most - 1) / most * mchunks + dma::kCUs - 1) / dma::kCUs;
@@ -432,16 +451,35 @@ hipError_t launch(const Params& p, hipStream_t s) {
     const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
     const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
     if (wgs >= (int64_t(1) << 32) / (NWAVE * 64)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w4_rows_kernel<T, LG, kGated, RBT>), dim3((unsigned)wgs), dim3(NWAVE * 64), 0,
-                       s, p, cols, (int)mchunks);
+    hipLaunchKernelGGL((w4_rows_kernel<T, LG, kGated, RBT, CBW>), dim3((unsigned)wgs), dim3(NWAVE * 64),
+                       0, s, p, cols, (int)mchunks);
     return hipGetLastError();
+}
+
+// Rows of activations by stored rows of a workgroup.  Its time does not depend on how many of them are
+// there: 27, 37 and 55 us for K = 8192 (groups of 128; 27 becomes 42 where a CU has two of the smallest, whose LDS and
+// registers allow that), so the tile is the one whose rounds of the CUs take least.  us, 32 x 64, 32 x 128 and 64 x 128
+// at K = 8192: 32 x 8192 28/37/52, 64 x 8192 28/38/56, 64 x 14336 43/39/56, 64 x 28672 83/76/59, 128 x 8192
+// 44/39/56, 256 x 8192 85/76/61, 256 x 3584 42/38/56.  (64 x 64 takes as long as 32 x 128.)
+enum class Tile { R32x64, R32x128, R64x128 };
+Tile tile_of(int64_t M, int64_t stored) {
+    auto wgs = [&](int rows, int strip) { return (M + rows - 1) / rows * ((stored + strip - 1) / strip); };
+    constexpr int64_t kCUs = dma::kCUs;
+    const int64_t small = wgs(32, 64), rest = small % (2 * kCUs);
+    const int64_t t32x64 = small / (2 * kCUs) * 42 + (rest == 0 ? 0 : rest <= kCUs ? 27 : 42);
+    const int64_t t32x128 = (wgs(32, 128) + kCUs - 1) / kCUs * 37;
+    const int64_t t64x128 = (wgs(64, 128) + kCUs - 1) / kCUs * 55;
+    if (t64x128 < t32x64 && t64x128 < t32x128) return Tile::R64x128;
+    return t32x128 < t32x64 ? Tile::R32x128 : Tile::R32x64;
 }
 
 template <In T, bool kGated>
 hipError_t launch_group(const Params& p, int log_group, hipStream_t s) {
+    const Tile tile = tile_of(p.M, (kGated ? 2 : 1) * (int64_t)p.N);
     auto rows = [&](auto lg) {
         constexpr int LG = decltype(lg)::value;
-        return p.M <= 32 ? launch<T, LG, kGated, 2>(p, s) : launch<T, LG, kGated, 4>(p, s);
+        if (tile == Tile::R64x128) return launch<T, LG, kGated, 4, 2>(p, s);
+        return tile == Tile::R32x128 ? launch<T, LG, kGated, 2, 2>(p, s) : launch<T, LG, kGated, 2, 1>(p, s);
     };
     return log_group == 5   ? rows(std::integral_constant<int, 0>{})
            : log_group == 6 ? rows(std::integral_constant<int, 1>{})

@@ -30,12 +30,12 @@ hipError_t launch_group(const strip::Params& p, hipStream_t s) {
 
 template <bool kGated>
 hipError_t launch_strips(In t, int log_group, const strip::Params& p, hipStream_t s) {
-    // Strips load the activations once per strip and wave: more than 16 rows take the kernel that
-    // shares them, where it has work for the CUs.  us, strips against it, K = 8192, group 128: 28672 x 32
-    // 44/43, x 64 80/63, x 256 285/232; 14336 x 32 39/38, x 64 71/55; 8192 x 32 29/37, x 64 51/54, x 128
-    // 92/56; 3584 x 64 43/54, x 128 82/54; gated 8192 x 32 39/39, x 64 69/55; gated 3584 x 64 50/55.
+    // Strips load the activations once per strip and wave: more rows take the kernel that shares
+    // them.  us, strips against it, K = 8192, groups of 128: 28672 x 32 44/41, x 64 80/59, x 256 285/228; 14336 x
+    // 32 39/29, x 64 71/39; 8192 x 32 29/28, x 48 41/28, x 64 51/28; 3584 x 32 24/28, x 48 34/28, x 64 43/27; 4096
+    // x 4096 x 32 15/16, x 64 27/16; gated 8192 x 32 39/29, gated 3584 x 32 28/28, x 64 50/28.
     const bool wide = (kGated ? 2 : 1) * (int64_t)p.N > 32 * dma::kCUs;
-    if ((p.M > 64 || (p.M > 16 && wide)) && rows_eligible(p))
+    if ((p.M > 32 || (p.M > 16 && wide)) && rows_eligible(p))
         return launch_rows(t, kGated, log_group, p, s);
     auto go = [&](auto tc) {
         constexpr In T = decltype(tc)::value;

@@ -185,3 +185,26 @@ def test_w4_many_rows_on_two_streams_and_in_graphs():
         torch.cuda.synchronize()
         assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
         work(x, outs())
+
+
+@pytest.mark.parametrize("M,N,K", [(400, 2561, 264), (33, 8212, 520), (65, 4100, 263), (513, 130, 1031), (40, 16400, 129), (64, 64, 300)])
+def test_w4_tiles_of_the_shared_kernel(M, N, K):
+    """Each of its tiles, plain and gated, with strips and blocks of rows that end inside them."""
+    rng = rng_for(M, N, K, 61)
+    for group in (32, 64, 128):
+        say("w4 tiles", M, N, K, group)
+        q, s, z = whole_weight(rng, N + N % 2, K, group, "f16", False)
+        s = s.abs().clamp(max=1)
+        z = rng.integers(6, 10, z.shape).astype(np.uint8)
+        X = torch.from_numpy((rng.random((M, K)) < min(1.0, 48 / K)) * rng.integers(-1, 2, (M, K)).astype(np.float32))
+        A, W = stored16(X, "bf16", -K % 8), on_gpu(q, s, z, True, 0)
+        p = X.double().cuda() @ torch.from_numpy(gp.values(q, s, z, group).T.copy()).cuda()
+        C = torch.full((M, len(q) + 1), 4.0, device="cuda")
+        dgt.check(dgt.gemm_w4(A, *W, C[:, :-1], group=group))
+        assert torch.equal(C[:, :-1].double(), p) and (C[:, -1] == 4.0).all()
+        F = len(q) // 2
+        H = torch.full((M, F + 1), 77.0, dtype=torch.bfloat16, device="cuda")
+        dgt.check(dgt.gated_w4(A, *W, H[:, :F], act="identity", group=group))
+        want = p[:, :F] * p[:, F:]
+        assert want.abs().max() < 2 ** 22
+        assert torch.equal(H[:, :F], want.bfloat16()) and (H[:, F] == 77.0).all()
