@@ -36,13 +36,18 @@ hipError_t launch_forward_strip(const Forward& p, hipStream_t s) {
     q.H = p.H; q.ldh = p.ldh;
     q.G = p.G; q.ldg = p.ldg;
     q.U = p.U; q.ldu = p.ldu;
-    // Strips of 16 outputs where there are few, of 32 and 64 where every CU has them (us, this rule and
-    // strips of 64 alone, K = 8192: 1 x 3584 21 and 30, 16 x 3584 22 and 34, 16 x 8192 55.4 and 57.4).
-    if (p.M > 32) return strip::launch<T, Cfg<4, 4, 32, 128>>(q, s);
-    if (p.M > 16) return strip::launch<T, Cfg<2, 8, 16, 256>>(q, s);
-    if (p.N <= 16 * dma::kCUs) return strip::launch<T, Cfg<1, 2, 16, 256>>(q, s);
-    if (p.N <= 32 * dma::kCUs) return strip::launch<T, Cfg<1, 4, 16, 256>>(q, s);
-    return strip::launch<T, Cfg<1, 8, 16, 256>>(q, s);
+    // Strips of 16 outputs where that gives every CU at most one, then of 32, then of 64.  us, this rule and
+    // strips of 64 alone, K = 8192: 1 x 3584 21 and 30, 16 x 3584 22 and 34, 32 x 3584 28 and 43, 64 x 3584 42 and
+    // 57, 16 x 8192 55 and 57, 32 x 8192 57 and 62, 64 x 8192 64 and 72 (strips of 16 there 83).
+    const bool few = p.N <= 16 * dma::kCUs, some = p.N <= 32 * dma::kCUs;
+    auto take = [&](auto narrow, auto middle, auto wide) {
+        return few    ? strip::launch<T, decltype(narrow)>(q, s)
+               : some ? strip::launch<T, decltype(middle)>(q, s)
+                      : strip::launch<T, decltype(wide)>(q, s);
+    };
+    if (p.M > 32) return take(Cfg<4, 2, 16, 128>{}, Cfg<4, 2, 32, 128>{}, Cfg<4, 4, 32, 128>{});
+    if (p.M > 16) return take(Cfg<2, 2, 16, 256>{}, Cfg<2, 4, 16, 256>{}, Cfg<2, 8, 16, 256>{});
+    return take(Cfg<1, 2, 16, 256>{}, Cfg<1, 4, 16, 256>{}, Cfg<1, 8, 16, 256>{});
 }
 template hipError_t launch_forward_strip<In::BF16>(const Forward&, hipStream_t);
 template hipError_t launch_forward_strip<In::F16>(const Forward&, hipStream_t);

@@ -208,3 +208,21 @@ def test_w4_tiles_of_the_shared_kernel(M, N, K):
         want = p[:, :F] * p[:, F:]
         assert want.abs().max() < 2 ** 22
         assert torch.equal(H[:, :F], want.bfloat16()) and (H[:, F] == 77.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("N", [33, 4097, 8200])
+@pytest.mark.parametrize("M,K", [(17, 520), (32, 1032), (33, 72), (64, 2056), (16, 8)])
+def test_gated_strips_of_every_width(M, N, K, dtype):
+    say("gated strips", M, N, K, dtype)
+    gen = gen_for(M, N, K, 67)
+    X, Wg, Wu = (stored16(ints(gen, r, K, top=1), dtype, 8) for r in (M, N, N))
+    b = ints(gen, 2, N).cuda()
+    H, h_ok = out_like(M, N, dtype, 1)
+    G, g_ok = out_like(M, N, dtype, 0, 1)
+    U, u_ok = out_like(M, N, dtype, 3)
+    dgt.check(dgt.gated(X, Wg, Wu, H, act="relu", bias_g=b[0], bias_u=b[1], G=G, U=U))
+    g, u = X.float() @ Wg.float().T + b[0], X.float() @ Wu.float().T + b[1]  # whole numbers: exact
+    assert torch.equal(G, g.to(DT[dtype])) and torch.equal(U, u.to(DT[dtype]))
+    assert torch.equal(H, (g.clamp(min=0) * u).to(DT[dtype]))
+    assert h_ok() and g_ok() and u_ok()
