@@ -130,14 +130,17 @@ __device__ __forceinline__ void read_weight(const uint32_t (&at)[BPW], const uin
 }
 
 // 2^LG blocks of 32 k a scale group; RBT blocks of 16 rows of activations, CBW of the weight a wave.
-template <In T, int LG, bool kGated, int RBT, int CBW>
-__global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int cols, int mchunks) {
+// kAny: rows of activations that start anywhere go through registers, loaded at a step's start and stored to
+// its end's free stage.
+template <In T, int LG, bool kGated, int RBT, int CBW, bool kAny>
+// (two workgroups a CU of the smallest tile: registers for four waves a SIMD)
+__global__ __launch_bounds__(NWAVE * 64, RBT * CBW == 2 ? 4 : 2) void w4_rows_kernel(Params p, int cols, int mchunks) {
     constexpr int GB = 1 << LG, GPS = STEPK / 32 / GB, GPW = GPS / KS, SPS = kRun / GPS;
     constexpr int ROWS = 16 * CBW * NWAVE / KS;      // stored rows of a strip
     constexpr int B_BYTES = ROWS * ROWB, IB = B_BYTES / 1024 / NWAVE;  // copies per wave
     constexpr int kPart = kGated ? ROWS / 2 : ROWS;  // stored rows of one matrix
     constexpr int A_BYTES = 16 * RBT * AROW, IA = A_BYTES / 1024 / NWAVE;
-    constexpr int STAGE = B_BYTES + A_BYTES, COPIES = IA + IB;
+    constexpr int STAGE = B_BYTES + A_BYTES, COPIES = (kAny ? 0 : IA) + IB;
     static_assert(A_BYTES % (1024 * NWAVE) == 0, "whole copies per wave");
     // One object per stage, so that the compiler's wait-count pass can tell a
     // copy into one from reads of another.
@@ -210,10 +213,39 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
         for (int j = 0; j < IB; ++j)
             copy_piece<2>(base_w[j], range_w, st + 1024 * (IB * wave + j),
                           cw[j] < lim_w ? voff_w[j] + (uint32_t)(ROWB * k) : 0xfffffff0u);
+        if (kAny) return;
 #pragma unroll
         for (int j = 0; j < IA; ++j)
             copy_piece<1>(base_x, range_x, st + B_BYTES + 1024 * (IA * wave + j),
                           cx[j] < lim_x ? voff_x[j] + (uint32_t)(AROW * k) : 0xfffffff0u);
+    };
+
+    // The same of the activations of any alignment: a piece that crosses a row's end or lies behind it is
+    // the row's last 8 elements, shifted (rows past the last one are that one, and not stored).
+    const uint16_t* row_x[IA];
+#pragma unroll
+    for (int j = 0; j < IA; ++j)
+        row_x[j] = p.X + (mbase + min(2 * (IA * wave + j) + lane / 32, rows_x - 1)) * p.ldx;
+    auto load_x = [&](int k, u32x4 (&v)[IA]) DGT_INLINE {
+        if (p.K < 8) {  // uniform; then there is one step
+#pragma unroll
+            for (int j = 0; j < IA; ++j)
+                v[j] = gated::gather8(row_x[j], STEPK * k + 8 * cx[j], p.K);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < IA; ++j)
+            v[j] = gated::load16(row_x[j] + min(STEPK * k + 8 * cx[j], p.K - 8));
+    };
+    auto store_x = [&](auto qc, int k, u32x4 (&v)[IA]) DGT_INLINE {
+        uint8_t* st = dma::pick<decltype(qc)::value>(st0, st1, st2, st0);
+        const bool cut = STEPK * (k + 1) > p.K && p.K >= 8;  // uniform
+#pragma unroll
+        for (int j = 0; j < IA; ++j) {
+            const int past = min(max(STEPK * k + 8 * cx[j] - (p.K - 8), 0), 8);
+            *reinterpret_cast<u32x4*>(st + B_BYTES + 1024 * (IA * wave + j) + 16 * lane) =
+                cut ? gated::shift_out(v[j], past) : v[j];
+        }
     };
 
     // Scales: lane tid's stored row.
@@ -232,22 +264,21 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
     };
     // A run's, or where the row ends in it the row's last ones.
     auto load_scales = [&](int run, Scales& o) DGT_INLINE {
-        if (few) {
-#pragma unroll
-            for (int d = 0; d < kRun / 2; ++d) o.s[d] = 0u;
-#pragma unroll
-            for (int d = 0; d < kRun / 4; ++d) o.z[d] = 0u;
-#pragma unroll
-            for (int e = 0; e + 1 < kRun; ++e)
-                if (e < p.groups) {
-                    o.s[e / 2] |= (uint32_t)srow[e] << (16 * (e % 2));
-                    o.z[e / 4] |= (uint32_t)zrow[p.Z[0] ? e : 0] << (8 * (e % 4));
-                }
-            return;
-        }
         const int at = min(kRun * run, p.groups - kRun);
         __builtin_memcpy(o.s, srow + at, 2 * kRun);
         __builtin_memcpy(o.z, zrow + (p.Z[0] ? at : 0), kRun);
+    };
+    auto load_few = [&](Scales& o) DGT_INLINE {
+#pragma unroll
+        for (int d = 0; d < kRun / 2; ++d) o.s[d] = 0u;
+#pragma unroll
+        for (int d = 0; d < kRun / 4; ++d) o.z[d] = 0u;
+#pragma unroll
+        for (int e = 0; e + 1 < kRun; ++e) {  // past the last group: it again, not used
+            const int at = min(e, p.groups - 1);
+            o.s[e / 2] |= (uint32_t)srow[at] << (16 * (e % 2));
+            o.z[e / 4] |= (uint32_t)zrow[p.Z[0] ? at : 0] << (8 * (e % 4));
+        }
     };
     const uint32_t smask = p.s_bf16 ? 0xffffffffu : 0u;
     // Into the run's buffer; past the row's last group scales of 0 (their sums are
@@ -349,7 +380,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
         constexpr int Q = decltype(qc)::value;
         DMA_WAIT_VMCNT_LGKM0(((NS - 2) * COPIES));
         dma::barrier();  // step s is in LDS for every wave; the stage of step s - 1 is free
-        if (p.K % 8 != 0 && now.k == nsteps - 1) {
+        if (!kAny && p.K % 8 != 0 && now.k == nsteps - 1) {
             // what follows k = K - 1 in the rows' last pieces may be anything
             if (tid < 16 * RBT) {
                 uint8_t* piece = dma::pick<Q>(st0, st1, st2, st0) + B_BYTES + tid * AROW +
@@ -361,15 +392,27 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
             dma::barrier();
         }
         Scales sc;
-        const bool last = now.r == SPS - 1 || now.k == nsteps - 1;  // of its run
+        // the last of its run, and there is another
+        const bool last = !few && (now.r == SPS - 1 || now.k == nsteps - 1);
         const int next = now.run + 1 == nruns ? 0 : now.run + 1;
         if (loads_scales && last) load_scales(next, sc);
         fence();
-        copy_step(std::integral_constant<int, (Q + NS - 1) % NS>{}, ahead.k, s + NS - 1 < nsteps);
+        constexpr std::integral_constant<int, (Q + NS - 1) % NS> next_stage{};
+        const int next_k = ahead.k;
+        u32x4 v[IA];
+        if constexpr (kAny) {
+            load_x(next_k, v);
+            fence();
+        }
+        copy_step(next_stage, next_k, s + NS - 1 < nsteps);
         advance(ahead);
         fence();
         const uint8_t* st = dma::pick<Q>(st0, st1, st2, st0);
         compute(st, now, buf);
+        if constexpr (kAny) {
+            fence();
+            store_x(next_stage, next_k, v);
+        }
         if (last) {
             buf ^= 1;
             if (loads_scales) put_scales(next, buf, sc);
@@ -379,11 +422,18 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
     };
     if (loads_scales) {
         Scales sc;
-        load_scales(now.run, sc);
+        if (few) load_few(sc);
+        else load_scales(now.run, sc);
         put_scales(now.run, 0, sc);
     }
     fence();
     static_for<NS - 1>([&](auto qc) DGT_INLINE {
+        if constexpr (kAny) {
+            u32x4 v[IA];
+            load_x(ahead.k, v);
+            store_x(qc, ahead.k, v);
+            fence();
+        }
         copy_step(qc, ahead.k, decltype(qc)::value < nsteps);
         advance(ahead);
     });
@@ -440,7 +490,7 @@ __global__ __launch_bounds__(NWAVE * 64, 1) void w4_rows_kernel(Params p, int co
     });
 }
 
-template <In T, int LG, bool kGated, int RBT, int CBW>
+template <In T, int LG, bool kGated, int RBT, int CBW, bool kAny = false>
 hipError_t launch(const Params& p, hipStream_t s) {
     constexpr int most = 16 * CBW * NWAVE / KS / (kGated ? 2 : 1);
     const int64_t mchunks = ((int64_t)p.M + 16 * RBT - 1) / (16 * RBT);
@@ -451,7 +501,7 @@ hipError_t launch(const Params& p, hipStream_t s) {
     const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
     const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
     if (wgs >= (int64_t(1) << 32) / (NWAVE * 64)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w4_rows_kernel<T, LG, kGated, RBT, CBW>), dim3((unsigned)wgs), dim3(NWAVE * 64),
+    hipLaunchKernelGGL((w4_rows_kernel<T, LG, kGated, RBT, CBW, kAny>), dim3((unsigned)wgs), dim3(NWAVE * 64),
                        0, s, p, cols, (int)mchunks);
     return hipGetLastError();
 }
@@ -476,8 +526,10 @@ Tile tile_of(int64_t M, int64_t stored) {
 template <In T, bool kGated>
 hipError_t launch_group(const Params& p, int log_group, hipStream_t s) {
     const Tile tile = tile_of(p.M, (kGated ? 2 : 1) * (int64_t)p.N);
+    const bool any = !rows_16b_aligned(p.X, p.ldx, 2) || p.ldx >= kMaxBufferPitch;
     auto rows = [&](auto lg) {
         constexpr int LG = decltype(lg)::value;
+        if (any) return launch<T, LG, kGated, 2, 1, true>(p, s);
         if (tile == Tile::R64x128) return launch<T, LG, kGated, 4, 2>(p, s);
         return tile == Tile::R32x128 ? launch<T, LG, kGated, 2, 2>(p, s) : launch<T, LG, kGated, 2, 1>(p, s);
     };
@@ -487,10 +539,6 @@ hipError_t launch_group(const Params& p, int log_group, hipStream_t s) {
 }
 
 }  // namespace
-
-bool rows_eligible(const Params& p) {
-    return p.K > 0 && rows_16b_aligned(p.X, p.ldx, 2) && p.ldx < kMaxBufferPitch;
-}
 
 hipError_t launch_rows(In t, bool gate, int log_group, const Params& p, hipStream_t s) {
     if (t == In::BF16)

@@ -10,16 +10,13 @@ namespace {
 using strip::Cfg;
 
 // 2^LG blocks of 32 k a scale group.  Strips of at most as many rows as give every CU one
-// (kGated: half as many outputs), wider ones where there are more rows than that: 16 to 128 rows
-// for up to 16 rows of activations, and up to 128 rows with two blocks of activations for more
-// (which is then only for activations that the shared kernel does not take).  us, with this rule and
+// (kGated: half as many outputs), wider ones where there are more rows than that: 16 to 128.  us, with this rule and
 // with strips of 128 rows alone, K = 8192, one row of activations: 3584 9.6 and 20.6, 8192 12.2 and 20.7,
 // 14336 15.6 and 21.4; gated 3584 12.0 and 20.1, 8192 17.4 and 22.6; 16 rows: 3584 14 and 25, 14336 21 and 28.
 template <In T, int LG, bool kGated>
 hipError_t launch_group(const strip::Params& p, hipStream_t s) {
     constexpr int kPair = kGated ? 2 : 1;
     constexpr int64_t kCUs = dma::kCUs;
-    if (p.M > 16 && p.N > 32 * kCUs) return strip::launch<T, Cfg<true, LG, kGated, 2, 4, 32, 128>>(p, s);
     if (p.N <= 16 * kCUs) return strip::launch<T, Cfg<true, LG, kGated, 1, kPair, 16, 128>>(p, s);
     if constexpr (!kGated) {
         if (p.N <= 32 * kCUs) return strip::launch<T, Cfg<true, LG, false, 1, 2, 16, 128>>(p, s);
@@ -35,7 +32,7 @@ hipError_t launch_strips(In t, int log_group, const strip::Params& p, hipStream_
     // 32 39/29, x 64 71/39; 8192 x 32 29/28, x 48 41/28, x 64 51/28; 3584 x 32 24/28, x 48 34/28, x 64 43/27; 4096
     // x 4096 x 32 15/16, x 64 27/16; gated 8192 x 32 39/29, gated 3584 x 32 28/28, x 64 50/28.
     const bool wide = (kGated ? 2 : 1) * (int64_t)p.N > 32 * dma::kCUs;
-    if ((p.M > 32 || (p.M > 16 && wide)) && rows_eligible(p))
+    if ((p.M > 32 || (p.M > 16 && wide)) && p.K > 0)
         return launch_rows(t, kGated, log_group, p, s);
     auto go = [&](auto tc) {
         constexpr In T = decltype(tc)::value;

@@ -322,11 +322,11 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
 #pragma unroll
             for (int d = 0; d < G::kRun / 4; ++d) o.z[j][d] = 0u;
 #pragma unroll
-            for (int e = 0; e + 1 < G::kRun; ++e)
-                if (e < p.groups) {
-                    o.s[j][e / 2] |= (uint32_t)srow[j][e] << (16 * (e % 2));
-                    o.z[j][e / 4] |= (uint32_t)zrow[j][p.Z[0] ? e : 0] << (8 * (e % 4));
-                }
+            for (int e = 0; e + 1 < G::kRun; ++e) {  // past the last group: it again, not used
+                const int at = min(e, p.groups - 1);
+                o.s[j][e / 2] |= (uint32_t)srow[j][at] << (16 * (e % 2));
+                o.z[j][e / 4] |= (uint32_t)zrow[j][p.Z[0] ? at : 0] << (8 * (e % 4));
+            }
         }
     };
 
@@ -658,8 +658,7 @@ hipError_t launch(const Params& p, hipStream_t s) {
 }  // namespace strip
 
 namespace w4 {
-// The kernel with shared activations (k_w4_rows.hip) and the operands it takes.
-bool rows_eligible(const strip::Params& p);
+// The kernel with shared activations (k_w4_rows.hip); K > 0.
 hipError_t launch_rows(In t, bool gate, int log_group, const strip::Params& p, hipStream_t s);
 }  // namespace w4
 
