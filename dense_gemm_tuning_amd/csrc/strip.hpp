@@ -70,8 +70,7 @@ struct Params {
 };
 
 // kW4: 4-bit weights, 2^LG blocks of 32 k a scale group.
-template <bool kW4_, int LG_, bool kGated_, int RB_, int NG_, int GR_, int ROWB_,
-          bool kSingle_ = (kW4_ && RB_ > 1)>
+template <bool kW4_, int LG_, bool kGated_, int RB_, int NG_, int GR_, int ROWB_>
 struct Cfg {
     static constexpr bool kW4 = kW4_, kGated = kGated_;
     static constexpr int RB = RB_, NG = NG_, GR = GR_, ROWB = ROWB_;
@@ -97,34 +96,27 @@ struct Cfg {
     // Vector loads per step besides the copies (those of scales where every
     // step has them; elsewhere they are not counted, which only waits for more).
     static constexpr int LA = RB * P + (SPS == 1 ? 2 * NSC : 0);
-    // Activations in one buffer, loaded again behind a step's last products (with
-    // more rows two do not fit the registers), or in two, a step ahead.
-    static constexpr bool kSingle = kSingle_;
     // Whether the activations' sums per scale group are made once a step and kept, or
     // (their registers are many when the scale groups are) the products with
     // the zero point are added up with those with the codes.
     static constexpr bool kKeepSums = RB * GPS <= 4;
     // rows of a reduction pass in one stage of all waves
     static constexpr int RR = STAGE / (ROWS * 4) < 16 ? STAGE / (ROWS * 4) : 16;
-    static_assert(ROWB == 256 || ROWB == 128 || ROWB == 64, "a row piece is 256, 128 or 64 bytes");
+    static_assert(ROWB == 256 || ROWB == 128, "a row piece is 256 or 128 bytes");
     static_assert(NG == 1 || NG == 2 || NG == 4 || NG == 8, "groups map onto the ring");
     static_assert(!kGated || NG % 2 == 0, "a gated strip's groups come in pairs");
     static_assert(!kW4 || P % GB == 0, "a scale group does not cross steps");
     static_assert(RR >= 4, "a pass holds an accumulator's rows");
     __device__ static int swz(int r) {  // 256 / ROWB rows share a line of all banks
-        return ROWB == 256 ? (r & 15) : ROWB == 128 ? ((r >> 1) & 7) : ((r >> 2) & 3);
+        return ROWB == 256 ? (r & 15) : ((r >> 1) & 7);
     }
     // Loads of operands behind the copy of group cp of the wave's step t, D phases
-    // before that group's wait: one in each phase 0 behind its copy, or with one buffer at
-    // the end of each step.  In the first kFirst steps some of those phases are the
-    // prologue, which loads before it copies (with one buffer, after).
+    // before that group's wait: one in each phase 0 behind its copy.  In the first kFirst steps
+    // some of those phases are the prologue, which loads before it copies.
     static constexpr int kFirst = NG >= D + 1 ? 0 : (D + NG - 1) / NG;
     static constexpr int loads(int cp, int t) {
         int n = 0;
-        for (int x = cp - D; x <= cp; ++x) {
-            if (kSingle) n += x < cp && x >= -t * NG - 1 && (x + 8 * NG) % NG == NG - 1;
-            else n += x >= -t * NG && x % NG == 0;
-        }
+        for (int x = cp - D; x <= cp; ++x) n += x >= -t * NG && x % NG == 0;
         return n;
     }
 };
@@ -512,7 +504,7 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
                 if ((s - s0) % G::SPS == 0) put_scales(s, sc);
                 fence();
             }
-            if constexpr (!G::kSingle) load_ops(s + 1, next);
+            load_ops(s + 1, next);
             if constexpr (kW4) {
                 if ((s + 1 - s0) % G::SPS == 0) load_scales(s + 1, sc);
             }
@@ -529,10 +521,6 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
         if constexpr (cp == 0) prepare(s, o);
         compute(qc, cpc, s, o);
         fence();
-        if constexpr (G::kSingle && cp == NG - 1) {  // o and next are one buffer
-            load_ops(s + 1, next);
-            fence();
-        }
     };
     // A step whose groups start at ring stage Q0.
     auto step = [&](auto q0c, int s, Ops& o, Ops& next, Scales& sc) DGT_INLINE {
@@ -545,45 +533,29 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
 
     if (s0 < s1) {
         Scales sc;
-        auto operands = [&](Ops& o) DGT_INLINE {
-            load_ops(s0, o);
-            if constexpr (kW4) {
-                load_scales(s0, sc);
-                if (few) load_few(sc);
-            }
-            fence();
-        };
-        auto copies = [&]() DGT_INLINE {
-            static_for<D>([&](auto dc) DGT_INLINE {
-                constexpr int d = decltype(dc)::value;
-                issue(dc, std::integral_constant<int, d % NG>{}, s0 + d / NG);
-            });
-            fence();
-        };
+        Ops o0, o1;
+        load_ops(s0, o0);
+        if constexpr (kW4) {
+            load_scales(s0, sc);
+            if (few) load_few(sc);
+        }
+        fence();
+        static_for<D>([&](auto dc) DGT_INLINE {
+            constexpr int d = decltype(dc)::value;
+            issue(dc, std::integral_constant<int, d % NG>{}, s0 + d / NG);
+        });
+        fence();
         // Unrolled so that ring stages and operand buffers are compile-time.
         constexpr int kRing = NS > NG ? NS / NG : 1;
-        constexpr int kUnroll = G::kSingle ? kRing : kRing > 2 ? kRing : 2;
-        auto run = [&](Ops& o0, Ops& o1) DGT_INLINE {
-            for (int s = s0; s < s1; s += kUnroll) {
-                static_for<kUnroll>([&](auto jc) DGT_INLINE {
-                    constexpr int j = decltype(jc)::value;
-                    if (s + j >= s1) return;
-                    using Q0 = std::integral_constant<int, (j * NG) % NS>;
-                    if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1, sc);
-                    else step(Q0{}, s + j, o1, o0, sc);
-                });
-            }
-        };
-        if constexpr (G::kSingle) {
-            Ops o;
-            copies();
-            operands(o);
-            run(o, o);
-        } else {
-            Ops o0, o1;
-            operands(o0);
-            copies();
-            run(o0, o1);
+        constexpr int kUnroll = kRing > 2 ? kRing : 2;
+        for (int s = s0; s < s1; s += kUnroll) {
+            static_for<kUnroll>([&](auto jc) DGT_INLINE {
+                constexpr int j = decltype(jc)::value;
+                if (s + j >= s1) return;
+                using Q0 = std::integral_constant<int, (j * NG) % NS>;
+                if constexpr (j % 2 == 0) step(Q0{}, s + j, o0, o1, sc);
+                else step(Q0{}, s + j, o1, o0, sc);
+            });
         }
     }
     DMA_WAIT_VMCNT_LGKM0(0);  // every copy has landed: the stages can be reused

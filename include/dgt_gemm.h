@@ -547,8 +547,8 @@ int gemm_w4_dequantize(int dtype, int group, int scale_dtype, int M, int K,
 
 /* C <- alpha*A*W^T + beta*C + bias with 16-bit A (`dtype`, M x K, any alignment)
  * and W the N x K operand Q, S, Z: for products of few rows (from a few hundred rows on,
- * gemm_w4_dequantize and a dense product are faster).  A on 16-byte rows with a pitch below
- * 2^24 takes the faster kernel above 32 rows (for wide weights above 16).  Weights are not rounded:
+ * gemm_w4_dequantize and a dense product are faster).  Above 16 rows A is read fastest
+ * from 16-byte rows with a pitch below 2^24.  Weights are not rounded:
  * within a group x*q and x are summed apart in fp32, and s*(sum xq - z*sum x) is
  * added up in fp32.  bias: NULL or N floats.  alpha == 0 or K == 0 reads neither
  * operand, beta == 0 does not read C. */
