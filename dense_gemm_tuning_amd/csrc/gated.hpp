@@ -137,9 +137,10 @@ __device__ __forceinline__ float act_at(Act act, float x, float& slope) {
         case Act::GeluTanh: {  // 0.5 * x * (1 + tanh(y/2)) = x * logistic(y)
             const float x2 = x * x;
             const Logistic s = logistic(kTanhA * x * fmaf(kTanhB, x2, 1.0f));
-            if (kSlope)  // x2 bounded: where it overflows, s.neg or s.pos is zero long since
-                slope = s.pos * fmaf(x * s.neg,
-                                     kTanhA * fmaf(3.0f * kTanhB, fminf(x2, 4096.0f), 1.0f), 1.0f);
+            if (kSlope) {  // x bounded: s.neg or s.pos is zero from |x| = 12 on, and products with x would overflow
+                const float b = fminf(fmaxf(x, -64.0f), 64.0f);
+                slope = s.pos * fmaf(b * s.neg, kTanhA * fmaf(3.0f * kTanhB, b * b, 1.0f), 1.0f);
+            }
             return x * s.pos;
         }
         case Act::Relu:
