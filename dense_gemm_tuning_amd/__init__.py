@@ -1028,7 +1028,8 @@ def gemm_w4(A, Q, S, Z, C, group: int = 128, alpha: float = 1.0, beta: float = 0
             stream=None) -> int:
     """C <- alpha*A*W^T + beta*C + bias with W the [N, K] weight in 4 bits Q, S, Z
     (Z None: zero points 8) and A [M, K] bfloat16 or float16 (gemm_w4_a16).  C is float32 [M, N],
-    row-major; bias None or float32 [N].  Returns the status code."""
+    row-major; bias None or float32 [N].  An infinity or NaN in A makes its row of C NaN.  Returns
+    the status code."""
     if C.dtype is not (_torch or _use_torch()).float32:
         raise TypeError("C must be float32")
     dtype = _code16(A, "A")
@@ -1050,8 +1051,8 @@ def gated_w4(X, Q, S, Z, H, act="silu", group: int = 128, bias_g=None, bias_u=No
              stream=None) -> int:
     """H <- act(X*Wg^T + bias_g) * (X*Wu^T + bias_u) with the weight in 4 bits Q, S, Z
     of 2N rows, Wg's and then Wu's (gemm_w4_gated).  X [M, K] and H [M, N] are both
-    bfloat16 or both float16, row-major; the biases float32 [N] or None.  Returns
-    the status code."""
+    bfloat16 or both float16, row-major; the biases float32 [N] or None.  An infinity or NaN in X
+    makes its row of H NaN.  Returns the status code."""
     dtype = _code16(X, "X")
     M, K, ldx = _matrix(X, "X")
     N = H.shape[1] if H.dim() == 2 else 0

@@ -3,7 +3,8 @@
 // written, or the other way round.
 //
 // Per group, over its elements and zero: with zero points s = (max - min)/15 and z the
-// whole number nearest to -min/s; without, s = max(max/7, -min/8) and z = 8.
+// whole number nearest to -min/s, at most 15 (s may have been rounded down); without,
+// s = max(max/7, -min/8) and z = 8.
 // The quotient that s is rounded from is taken in 64 bits; s is rounded to fp32, then
 // to its 16-bit type (past that type's largest value: that value).  q = the
 // whole number nearest to x/s, ties to even, plus z, within 0 .. 15.

@@ -529,7 +529,7 @@ int64_t gemm_gated_grad_workspace_size(int M, int N);
 
 /* Q, S, Z <- the M x K matrix X in the input format `dtype`, any alignment.
  * Per group, over its elements and 0: with Z, s = (max - min)/15 and
- * z = -min/s to the nearest whole number; with Z == NULL, s = max(max/7, -min/8).
+ * z = -min/s to the nearest whole number, at most 15; with Z == NULL, s = max(max/7, -min/8).
  * s is rounded to fp32 and then to its type (past the type's largest value: that
  * value); x becomes the whole number nearest to x/s (ties to even) plus z, within
  * 0 .. 15.  A group whose scale comes out as 0 gets the code z.  A
@@ -550,7 +550,10 @@ int gemm_w4_dequantize(int dtype, int group, int scale_dtype, int M, int K,
  * gemm_w4_dequantize and a dense product are faster).  Above 16 rows A is read fastest
  * from 16-byte rows with a pitch below 2^24.  Weights are not rounded:
  * within a group x*q and x are summed apart in fp32, and s*(sum xq - z*sum x) is
- * added up in fp32.  bias: NULL or N floats.  alpha == 0 or K == 0 reads neither
+ * added up in fp32.  So the error goes by the sizes of s*q*x and s*z*x, also where the
+ * two sums cancel; an infinite or NaN x makes its whole row of C (of H below) NaN; and a
+ * group whose |x| add up to 2^119 or more, as only BF16 can, may become infinite or NaN
+ * though s*(q - z)*x are not.  bias: NULL or N floats.  alpha == 0 or K == 0 reads neither
  * operand, beta == 0 does not read C. */
 int gemm_w4_a16(int dtype, int group, int scale_dtype, int M, int N, int K,
                 float alpha, const uint16_t* A, int lda, const uint8_t* Q, int ldq,
