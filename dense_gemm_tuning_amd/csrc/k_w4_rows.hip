@@ -23,8 +23,6 @@
 // sums made once for the four waves that share them, and subtracted a step later, took 65.)
 // Rows of activations off 16-byte boundaries (or with pitches from 2^24 on) go through registers, on the
 // smallest tile: 28672 x 8192, 32 rows 52 us, 64 106, 256 342.
-#include <algorithm>
-
 #include "strip.hpp"
 
 namespace dgt {
@@ -135,7 +133,7 @@ __device__ __forceinline__ void read_weight(const uint32_t (&at)[BPW], const uin
 // to the free stage at its end.
 template <In T, int LG, bool kGated, int RBT, int CBW, bool kAny>
 // (two workgroups a CU of the smallest tile: registers for four waves a SIMD)
-__global__ __launch_bounds__(NWAVE * 64, RBT * CBW == 2 ? 4 : 2) void w4_rows_kernel(Params p, int cols, int mchunks) {
+__global__ __launch_bounds__(NWAVE * 64, RBT * CBW == 2 ? 4 : 2) void w4_rows_kernel(Params p, int mchunks) {
     constexpr int GB = 1 << LG, GPS = STEPK / 32 / GB, GPW = GPS / KS, SPS = kRun / GPS;
     constexpr int ROWS = 16 * CBW * NWAVE / KS;      // stored rows of a strip
     constexpr int B_BYTES = ROWS * ROWB, IB = B_BYTES / 1024 / NWAVE;  // copies per wave
@@ -157,9 +155,9 @@ __global__ __launch_bounds__(NWAVE * 64, RBT * CBW == 2 ? 4 : 2) void w4_rows_ke
     const int wk = wave % KS, wc = wave / KS;
     // the row chunks of one strip on one XCD, as in strip.hpp
     const int q8 = blockIdx.x / (8 * mchunks), r8 = blockIdx.x % (8 * mchunks);
-    const int64_t first = (int64_t)(8 * q8 + r8 % 8) * cols;
+    const int64_t first = (int64_t)(8 * q8 + r8 % 8) * kPart;
     if (first >= p.N) return;
-    const int n0 = (int)first, nlim = (int)min(first + cols, (int64_t)p.N);
+    const int n0 = (int)first, nlim = min(n0 + kPart, p.N);
     const int mbase = (r8 / 8) * 16 * RBT;
     const int rows_x = min(16 * RBT, p.M - mbase);
     const int nsteps = (p.chunks + CPS - 1) / CPS, nruns = (nsteps + SPS - 1) / SPS;
@@ -493,25 +491,24 @@ __global__ __launch_bounds__(NWAVE * 64, RBT * CBW == 2 ? 4 : 2) void w4_rows_ke
 
 template <In T, int LG, bool kGated, int RBT, int CBW, bool kAny = false>
 hipError_t launch(const Params& p, hipStream_t s) {
-    constexpr int most = 16 * CBW * NWAVE / KS / (kGated ? 2 : 1);
+    constexpr int kCols = 16 * CBW * NWAVE / KS / (kGated ? 2 : 1);  // outputs of a strip
     const int64_t mchunks = ((int64_t)p.M + 16 * RBT - 1) / (16 * RBT);
-    // as narrow as the rounds of the CUs that the widest strips take allow
-    const int64_t rounds = (((int64_t)p.N + most - 1) / most * mchunks + dma::kCUs - 1) / dma::kCUs;
-    const int64_t per = std::max<int64_t>(1, rounds * dma::kCUs / mchunks);
-    const int cols = (int)std::min<int64_t>(most, ((int64_t)p.N + per - 1) / per);
-    const int64_t strips = ((int64_t)p.N + cols - 1) / cols;
+    const int64_t strips = ((int64_t)p.N + kCols - 1) / kCols;
     const int64_t wgs = (strips + 7) / 8 * 8 * mchunks;
     if (wgs >= (int64_t(1) << 32) / (NWAVE * 64)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((w4_rows_kernel<T, LG, kGated, RBT, CBW, kAny>), dim3((unsigned)wgs), dim3(NWAVE * 64),
-                       0, s, p, cols, (int)mchunks);
+                       0, s, p, (int)mchunks);
     return hipGetLastError();
 }
 
 // Rows of activations by stored rows of a workgroup.  Its time does not depend on how many of them are
 // there: 27, 37 and 55 us for K = 8192 (groups of 128; 27 becomes 42 where a CU has two of the smallest, whose LDS and
-// registers allow that), so the tile is the one whose rounds of the CUs take least.  us, 32 x 64, 32 x 128 and 64 x 128
-// at K = 8192: 32 x 8192 28/37/52, 64 x 8192 28/38/56, 64 x 14336 43/39/56, 64 x 28672 83/76/59, 128 x 8192
-// 44/39/56, 256 x 8192 85/76/61, 256 x 3584 42/38/56.  (64 x 64 takes as long as 32 x 128.)
+// registers allow that), so the tile is the one whose rounds of the CUs take least, and its strips are not narrowed where
+// CUs are idle (narrowed against whole strips, us: 33 x 129 27.7/26.7, 64 x 3584 28.1/27.5, 64 x 28672 59.5/60.0).
+// us, 32 x 64, 32 x 128 and 64 x 128 at K = 8192: 32 x 8192 28/37/52, 64 x 8192 28/38/56, 64 x 14336 43/39/56, 64 x 28672
+// 83/76/59, 128 x 8192 44/39/56, 256 x 8192 85/76/61, 256 x 3584 42/38/56.  (64 x 64 takes as long as 32 x 128.)  Groups of
+// 32 take longer at every tile and rank them alike: 64 x 8192 31/49/72, 64 x 14336 53/55/76, 64 x 28672 104/105/81,
+// 128 x 8192 53/54/76, 256 x 8192 100/104/77, 256 x 3584 51/52/74; so do groups of 64, in between.
 enum class Tile { R32x64, R32x128, R64x128 };
 Tile tile_of(int64_t M, int64_t stored) {
     auto wgs = [&](int rows, int strip) { return (M + rows - 1) / rows * ((stored + strip - 1) / strip); };
