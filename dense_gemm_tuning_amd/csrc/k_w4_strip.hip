@@ -11,7 +11,7 @@ using strip::Cfg;
 
 // 2^LG blocks of 32 k a scale group.  Strips of at most as many rows as give every CU one
 // (kGated: half as many outputs), wider ones where there are more rows than that: 16 to 128.  us, with this rule and
-// with strips of 128 rows alone, K = 8192, one row of activations: 3584 9.6 and 20.6, 8192 12.2 and 20.7,
+// with strips of 128 rows alone, K = 8192, one row of activations: 3584 8.8 and 20.6, 8192 12.2 and 20.7,
 // 14336 15.6 and 21.4; gated 3584 12.0 and 20.1, 8192 17.4 and 22.6; 16 rows: 3584 14 and 25, 14336 21 and 28.
 template <In T, int LG, bool kGated>
 hipError_t launch_group(const strip::Params& p, hipStream_t s) {

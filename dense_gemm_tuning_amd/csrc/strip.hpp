@@ -120,11 +120,11 @@ struct Cfg {
         return n;
     }
 };
-static_assert(Cfg<true, 2, false, 1, 4, 32, 128>::kFirst == 0 &&
-                  Cfg<true, 2, false, 1, 4, 32, 128>::loads(0, 0) == 1 &&
-                  Cfg<true, 2, false, 1, 4, 32, 128>::loads(3, 0) == 1 &&
-                  Cfg<true, 2, false, 1, 2, 32, 128>::loads(1, 0) == 1 &&
-                  Cfg<true, 2, false, 1, 2, 32, 128>::loads(0, 2) == 2 &&
+static_assert(Cfg<true, 2, false, 1, 4, 16, 128>::kFirst == 0 &&
+                  Cfg<true, 2, false, 1, 4, 16, 128>::loads(0, 0) == 1 &&
+                  Cfg<true, 2, false, 1, 4, 16, 128>::loads(3, 0) == 1 &&
+                  Cfg<true, 2, false, 1, 2, 16, 128>::loads(1, 0) == 1 &&
+                  Cfg<true, 2, false, 1, 2, 16, 128>::loads(0, 2) == 2 &&
                   Cfg<true, 2, false, 1, 1, 16, 128>::kFirst == 3 &&
                   Cfg<true, 2, false, 1, 1, 16, 128>::loads(0, 3) == 4 &&
                   Cfg<false, 0, true, 1, 8, 16, 256>::loads(4, 0) == 0,
@@ -613,7 +613,8 @@ __global__ __launch_bounds__(NW * 64, 1) void strip_kernel(Params p, int cols, i
 }
 
 // Strips as narrow as the number of rounds of the CUs (a workgroup each) that the widest
-// would take allows.
+// would take allows.  us, so and whole strips, K = 8192: 16-bit gated 1 x 1000 12.1/14.1, 1 x 3584 20.7/20.5, 8 x 9000
+// 48/52, 8 x 28672 139/149, 64 x 28672 173/182; 4-bit 1 x 3584 8.8/9.4, 1 x 14336 15.7/15.2, 8 x 28672 27.5/28.6.
 template <In T, typename G>
 hipError_t launch(const Params& p, hipStream_t s) {
     const int64_t mchunks = ((int64_t)p.M + 16 * G::RB - 1) / (16 * G::RB);

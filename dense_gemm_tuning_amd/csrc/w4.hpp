@@ -1,6 +1,6 @@
 // w4.hpp -- weights in 4 bits with a 16-bit scale (and a zero point) per group:
 // the layout shared by the kernels (k_w4_*.hip) and their entry points
-// (w4_api.cpp).
+// (gated_api.cpp).
 //
 // A row of K elements is ceil(K/group) groups of `group` (32, 64 or 128)
 // consecutive k with one scale s and one zero point z (8 where none is stored); element
