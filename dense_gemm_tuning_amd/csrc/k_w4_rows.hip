@@ -22,7 +22,9 @@
 // 32 KB of activations and 16 KB of codes); without the sums of x, a third of the products, 52.  (Those
 // sums made once for the four waves that share them, and subtracted a step later, took 65.)
 // Rows of activations off 16-byte boundaries (or with pitches from 2^24 on) go through registers, on the
-// smallest tile: 28672 x 8192, 32 rows 52 us, 64 106, 256 342.
+// smallest tile: 28672 x 8192, 32 rows 52 us, 64 93, 256 322.  Tiles of 32 x 128 and 64 x 128 through registers, timed
+// but not built, are faster where there is work for them (28672 x 8191, 32 x 64, 32 x 128 and 64 x 128, us: 32 rows
+// 55/50/71, 64 102/92/68, 256 330/300/264; 64 x 3584 37/43/63).
 #include "strip.hpp"
 
 namespace dgt {
