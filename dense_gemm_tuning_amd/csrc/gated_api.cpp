@@ -313,12 +313,23 @@ int gemm_w4_gated(int dtype, int act, int group, int scale_dtype, int M, int N, 
         share(h, weight_rows(2 * N, K, lg, Q, ldq, S, lds, Z, ldz)) ||
         share(h, rows_of(bias_g, 1, N, N, 4)) || share(h, rows_of(bias_u, 1, N, N, 4)))
         return GEMM_ERR_OVERLAP;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (K == 0) {  // the biases alone: no weights, whatever their type
+        gated::Forward f = {};
+        f.act = p.act;
+        f.M = M; f.N = N;
+        f.ldx = ldx; f.ldwg = f.ldwu = 1;
+        f.bg = bias_g; f.bu = bias_u;
+        f.H = H; f.ldh = ldh;
+        return status_of(t == DType::BF16 ? gated::launch_forward<dgt::In::BF16>(f, s)
+                                          : gated::launch_forward<dgt::In::F16>(f, s));
+    }
     p.M = M; p.N = N; p.K = K;
     p.X = X; p.ldx = ldx;
     p.w = weight_of(Q, ldq, S, lds, Z, ldz, bf16, lg);
     p.bg = bias_g; p.bu = bias_u;
     p.H = H; p.ldh = ldh;
-    return status_of(w4::launch_gated(in_of(t), p, static_cast<hipStream_t>(stream)));
+    return status_of(w4::launch_gated(in_of(t), p, s));
 }
 
 }  // extern "C"

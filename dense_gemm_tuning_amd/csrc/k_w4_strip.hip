@@ -32,8 +32,7 @@ hipError_t launch_strips(In t, int log_group, const strip::Params& p, hipStream_
     // 32 39/29, x 64 71/39; 8192 x 32 29/28, x 48 41/28, x 64 51/28; 3584 x 32 24/28, x 48 34/28, x 64 43/27; 4096
     // x 4096 x 32 15/16, x 64 27/16; gated 8192 x 32 39/29, gated 3584 x 32 28/28, x 64 50/28.
     const bool wide = (kGated ? 2 : 1) * (int64_t)p.N > 32 * dma::kCUs;
-    if ((p.M > 32 || (p.M > 16 && wide)) && p.K > 0)
-        return launch_rows(t, kGated, log_group, p, s);
+    if (p.M > 32 || (p.M > 16 && wide)) return launch_rows(t, kGated, log_group, p, s);
     auto go = [&](auto tc) {
         constexpr In T = decltype(tc)::value;
         return log_group == 5   ? launch_group<T, 0, kGated>(p, s)

@@ -631,7 +631,7 @@ hipError_t launch(const Params& p, hipStream_t s) {
 }  // namespace strip
 
 namespace w4 {
-// The kernel with shared activations (k_w4_rows.hip); K > 0.
+// The kernel with shared activations (k_w4_rows.hip).
 hipError_t launch_rows(In t, bool gate, int log_group, const strip::Params& p, hipStream_t s);
 }  // namespace w4
 

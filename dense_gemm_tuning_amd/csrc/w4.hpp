@@ -30,7 +30,7 @@ inline int groups(int K, int log_group) {
     return (int)(((int64_t)K + (1 << log_group) - 1) >> log_group);
 }
 
-struct Product {  // C <- alpha*A*W^T + beta*C + bias
+struct Product {  // C <- alpha*A*W^T + beta*C + bias; K > 0, as in Gated
     int M, N, K;
     float alpha, beta;
     const uint16_t* A;

@@ -472,7 +472,8 @@ enum gemm_activation {
  * and U must not overlap each other or an input (GEMM_ERR_OVERLAP; column
  * ranges of one matrix, with one pitch, do not overlap).  Checks run in this order:
  * dtype and activation, dimensions, pitches, quick return for an empty H, null
- * pointers, overlap. */
+ * pointers, overlap.  A call that needs more workgroups than one launch holds (2^32
+ * threads: from 2^24 tiles of 128 rows by 64 columns on) is GEMM_ERR_DIM. */
 int gemm_gated(int dtype, int act, int M, int N, int K, const uint16_t* X, int ldx,
                const uint16_t* Wg, int ldwg, const uint16_t* Wu, int ldwu,
                const float* bias_g, const float* bias_u, uint16_t* H, int ldh,
@@ -525,7 +526,9 @@ int64_t gemm_gated_grad_workspace_size(int M, int N);
  *             everywhere (ldz is not looked at)
  *
  * Checks run in this order: dtypes, activation and group, dimensions, pitches,
- * quick return for an empty result, null pointers, alignment, overlap. */
+ * quick return for an empty result, null pointers, alignment, overlap.  A product that needs
+ * more workgroups than one launch holds (2^32 threads: from 2^23 strips of 32 rows by 64
+ * rows of the weight on, counted eight at a time along the weight) is GEMM_ERR_DIM. */
 
 /* Q, S, Z <- the M x K matrix X in the input format `dtype`, any alignment.
  * Per group, over its elements and 0: with Z, s = (max - min)/15 and

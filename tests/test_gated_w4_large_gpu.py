@@ -194,3 +194,16 @@ def test_packing_more_than_2_to_31_elements():
     for r in rows_of(M):
         step = S[r].float().repeat_interleave(128, 1)[:, :K]
         assert ((Y[r].float() - X[r].float()).abs() <= 1.01 * step + 2.0 ** -8 * X[r].float().abs()).all(), r
+
+
+def test_no_k_and_many_rows():
+    """Without weights there is a bias per column, whatever the number of rows."""
+    M, N = (1 << 22) + 5, 100
+    say("gated_w4 without k", M, N)
+    none = [torch.empty(2 * N, 0, dtype=t, device="cuda") for t in (torch.uint8, F16, torch.uint8)]
+    X = torch.empty(M, 0, dtype=F16, device="cuda")
+    b = torch.arange(N, dtype=torch.float32, device="cuda")
+    for dtype in (F16, BF):
+        H = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+        dgt.check(dgt.gated_w4(X.to(dtype), *none, H, act="relu", group=64, bias_g=b, bias_u=b * 0 + 2))
+        assert torch.equal(H, (2 * b).to(dtype).expand(M, N))
